@@ -485,6 +485,118 @@ int std_dense_verify_attn_noalloc(const std_dims* dims, const void* q, int gamma
 int std_accept_prefix(int B, int gamma, const int32_t* draft, const int32_t* dense_argmax,
                       int32_t* n_plus_1, int32_t* accepted, std_stream_t stream);
 
+/* ---------------------------------------------------------------- queries and rows of new tokens
+ *
+ * No counterpart in the summary (its method starts from queries and keys): what a layer does
+ * between its projections and the calls of this library, in one pass -- an RMS norm of every query
+ * and key head, the position rotation, the change from token-major to head-major layout, and the
+ * append of the K and V rows to a cache.
+ */
+
+/* The rotation.  The first rot_dim channels of a head are rot_dim / 2 pairs; pair i is channels
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when `interleaved`, and turns by
+ * t = position * inv_freq[i]:  (a, b) -> (a cos t - b sin t, b cos t + a sin t).
+ * A video's tokens may have a position on up to three axes (frame, row, column): the first
+ * section[0] pairs turn with axis 0, the next section[1] with axis 1, the others with axis 2. */
+typedef struct std_rope {
+  const double* inv_freq; /* device [rot_dim / 2], radians for one position step */
+  int32_t rot_dim;        /* 0 (no rotation) .. d, a multiple of d / 8 */
+  int32_t interleaved;    /* 0 or 1 */
+  int32_t n_axes;         /* 1, 2 or 3 */
+  int32_t section[3];     /* pairs of each axis; the first n_axes entries sum to rot_dim / 2 */
+} std_rope;
+
+/* For every token r < n_rows[b] of every sequence b and layer l:
+ *   q_out row  <- rotate(norm(q_in, q_weight[l]))
+ *   cache row len[b] + pos_offset + r of k_cache <- rotate(norm(k_in, k_weight[l])), of v_cache <- v_in
+ *   norm(x, w)_i = w_i x_i / sqrt(mean_j x_j^2 + eps)
+ * Norm, angles (64-bit) and rotation are rounded once, to the output type.
+ * q_in      [L][B][rows][Hq][d], k_in and v_in [L][B][rows][Hkv][d], of dims->dtype; neighbouring
+ *           tokens are q_stride / k_stride / v_stride ELEMENTS apart (so a fused projection's
+ *           output serves: stride (Hq + 2 Hkv) d), at least heads * d and a multiple of 16 bytes.
+ *           Any of the three may be NULL, with its output: that part is left out.
+ * rows      tokens of each sequence in the buffers; n_rows (device int32 [B], or NULL: rows each)
+ *           those that are valid.  Nothing is read or written for the others.
+ * q_weight, k_weight  [L][d] of dims->dtype, or NULL: no norm of that part
+ * pos       device int32 [n_axes][B][rows], or NULL (one axis): the token's cache position
+ * q_out     [L][B][Hq][rows][d];  k_cache, v_cache  [L][B][Hkv][cap][d];  len  device int32 [B]
+ *           (may be NULL when k_in and v_in are and `pos` is given)
+ * A sequence whose rows would pass `cap` is skipped and flags STD_DEVERR_CAPACITY; one with n_rows[b]
+ * outside [0, rows] flags STD_DEVERR_LENGTH.  Lengths are not changed.  Inputs and outputs must not
+ * overlap.  rows = 0 does nothing. */
+int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_in, int64_t q_stride, const void* k_in,
+                     int64_t k_stride, const void* v_in, int64_t v_stride, int rows, const int32_t* n_rows,
+                     const void* q_weight, const void* k_weight, float eps, const int32_t* pos, void* q_out,
+                     void* k_cache, void* v_cache, int64_t cap, const int32_t* len, int pos_offset,
+                     std_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit K/V cache
+ *
+ * Not the method's selection: a second way to make the draft cheap, or a cache of its own.  The
+ * draft may attend a 4-bit copy of the whole context (144 bytes a row and head of K and V at d = 128,
+ * 512 in bf16) instead of a top-K subset; verification over the full cache keeps the output that of
+ * dense decoding.
+ *
+ * A row is d / 64 groups of 64 channels (d = 64 or 128), each with a bfloat16 scale s and minimum m:
+ *   m = bf16(min x),  s = bf16(float(max x - m) / 15),  c = clamp(round(float(x - m) / s), 0, 15)
+ * (ties to even; the quotient is rounded as if it were exact), and code c stands for m + c s.  A group
+ * with an infinity or a NaN, or wider than fp32 can hold, reads back as NaN in all its channels; one
+ * whose s is 0 reads back as m.
+ *   codes   [L][B][Hkv][cap][d / 2] bytes: 32-bit words of 8 channels, channel 8 j + n of a group in
+ *           bits [4 n, 4 n + 4) of its word j; at d = 128 word 2 j of a row is group 0's word j, word
+ *           2 j + 1 group 1's
+ *   scales  [L][B][Hkv][cap][d / 64][2] bfloat16: s, m
+ * cap is a multiple of 16; all four arrays are 16-byte aligned.
+ */
+typedef struct std_kv4_cache {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int64_t cap;
+} std_kv4_cache;
+
+/* std_kv_append into a 4-bit cache: n_new rows per (layer, sequence, KV head), k_new / v_new
+ * [L][B][Hkv][n_new][d] of dims->dtype, at rows len[b] + pos_offset + r.  Lengths are not changed.
+ * A sequence whose rows would pass the capacity is skipped and flags STD_DEVERR_CAPACITY.  n_new = 0 (and
+ * max_n = 0 below) does nothing. */
+int std_kv4_append(const std_dims* dims, const std_kv4_cache* cache, const int32_t* len, int pos_offset,
+                   const void* k_new, const void* v_new, int n_new, std_stream_t stream);
+
+/* Rows of a full cache into the same rows of a 4-bit one: rows [begin[b], begin[b] + count[b]) of
+ * k_full / v_full [L][B][Hkv][cap_full][d].  begin device int32 [B] or NULL (0); count device int32 [B]
+ * or NULL (max_n); max_n bounds every count[b] and sizes the launch.  After the prefill: begin NULL,
+ * count the committed lengths; after a verify: begin the committed length before it, count the
+ * accepted inputs (n_plus_1).  A sequence whose rows pass either capacity, or with count[b] outside
+ * [0, max_n], is skipped and flags STD_DEVERR_CAPACITY. */
+int std_kv4_quantize(const std_dims* dims, const std_kv4_cache* cache, const void* k_full, const void* v_full,
+                     const int32_t* begin, const int32_t* count, int max_n, std_stream_t stream);
+
+/* The values that rows [begin[b], begin[b] + count[b]) stand for, into rows [0, count[b]) of k_out / v_out
+ * [L][B][Hkv][max_n][d] of dims->dtype; other rows are left as they are.  Arguments and checks as above. */
+int std_kv4_read(const std_dims* dims, const std_kv4_cache* cache, const int32_t* begin, const int32_t* count,
+                 int max_n, void* k_out, void* v_out, std_stream_t stream);
+
+/* Device workspace bytes of std_kv4_attn for q_rows query rows over a cache of `cap` rows on the
+ * current device; 0 when the arguments are invalid. */
+size_t std_kv4_attn_workspace_size(const std_dims* dims, int q_rows, int64_t cap);
+
+/* Decode attention over a 4-bit cache.  Query row i < q_rows of each query head attends causally:
+ *     o_i = softmax_j(q_i . k_j / sqrt(d)) v_j   over cache rows j < len[b] + len_offset + i
+ * (q_rows = 1 and len_offset = rows appended since: a draft step, as std_sparse_decode_attn;
+ * q_rows = gamma + 1 and len_offset = 1: verify rows, as std_dense_verify_attn).
+ * q  [L][B][Hq][q_rows][d] and o  [L][B][Hq][q_rows][d], both of dims->dtype: unlike the calls above,
+ *    o comes in the queries' type, the type the layer's output projection reads
+ * len  device int32 [B]; len[b] < 0, or len[b] + len_offset + q_rows - 1 beyond the capacity, flags
+ *    STD_DEVERR_LENGTH and leaves that sequence's o as it is.  A row that attends no key gets o = 0.
+ * Keys, values, softmax statistics and sums are those of the cache's values in float32 arithmetic; for
+ * bf16 queries a weight is rounded once to 11 bits where it enters the tensor cores, for fp32 queries
+ * it and the query keep 22.
+ * Requires 1 <= q_rows <= 32, G * q_rows <= 128, B <= 1024, d 64 or 128.  The workspace needs no
+ * initial value; calls that may overlap on the device need workspaces of their own. */
+int std_kv4_attn(const std_dims* dims, const void* q, int q_rows, const std_kv4_cache* cache, const int32_t* len,
+                 int len_offset, void* o, void* ws, size_t ws_bytes, std_stream_t stream);
+
 /* ---------------------------------------------------------------- cache bookkeeping */
 
 /* Write `n_new` rows per (layer, sequence, KV head) into a cache at positions

@@ -62,7 +62,17 @@ class StdRoundIO(ctypes.Structure):
                 ("o_draft", _P), ("o_verify", _P), ("n_plus_1", _P), ("accepted", _P)]
 
 
+class StdRope(ctypes.Structure):
+    _fields_ = [("inv_freq", _P), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("section", ctypes.c_int32 * 3)]
+
+
+class StdKv4Cache(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("cap", _I64)]
+
+
 _DP = ctypes.POINTER(StdDims)
+_KP = ctypes.POINTER(StdKv4Cache)
 SIGNATURES = {
     "std_version": (_I, []),
     "std_launch_count": (ctypes.c_ulonglong, []),
@@ -96,6 +106,13 @@ SIGNATURES = {
     "std_accept_prefix": (_I, [_I, _I, _P, _P, _P, _P, _P]),
     "std_kv_append": (_I, [_DP, _P, _P, _I64, _P, _I, _P, _P, _I, _P]),
     "std_kv_commit": (_I, [_DP, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "std_qk_norm_rope": (_I, [_DP, ctypes.POINTER(StdRope), _P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _P,
+                              ctypes.c_float, _P, _P, _P, _P, _I64, _P, _I, _P]),
+    "std_kv4_append": (_I, [_DP, _KP, _P, _I, _P, _P, _I, _P]),
+    "std_kv4_quantize": (_I, [_DP, _KP, _P, _P, _P, _P, _I, _P]),
+    "std_kv4_read": (_I, [_DP, _KP, _P, _P, _I, _P, _P, _P]),
+    "std_kv4_attn_workspace_size": (_SZ, [_DP, _I, _I64]),
+    "std_kv4_attn": (_I, [_DP, _P, _I, _KP, _P, _I, _P, _P, _SZ, _P]),
     "std_round_workspace_size": (_SZ, [_DP, _I, _I, _I]),
     "std_probe_exp2": (_I, [_P, _P, _P, _I, _P]),
     "std_probe_wait_timeout": (_I, [_P, _P]),
@@ -356,6 +373,80 @@ def std_kv_append(d: StdDims, k_cache, v_cache, cap, length, pos_offset, k_new, 
                   stream=None) -> None:
     _check(lib().std_kv_append(ctypes.byref(d), _ptr(k_cache), _ptr(v_cache), cap, _ptr(length), pos_offset,
                                _ptr(k_new), _ptr(v_new), n_new, _stream(stream)))
+
+
+# new tokens' queries and rows
+
+def std_rope(inv_freq, sections=None, interleaved=False) -> StdRope:
+    """The rotation: inv_freq a float64 CUDA tensor [rot_dim / 2] (kept alive by the result), or None
+    (no rotation); sections the pairs of each position axis (default: one axis has them all)."""
+    if inv_freq is not None and str(inv_freq.dtype) != "torch.float64":
+        raise ValueError("inv_freq must be a float64 tensor")
+    half = 0 if inv_freq is None else inv_freq.numel()
+    sections = [half] if sections is None else [int(x) for x in sections]
+    if not 1 <= len(sections) <= 3:
+        raise ValueError("one to three sections")
+    r = StdRope(_ptr(inv_freq), 2 * half, int(interleaved), len(sections),
+                (ctypes.c_int32 * 3)(*(sections + [0] * (3 - len(sections)))))
+    r.keep = inv_freq
+    return r
+
+
+def _tokens(x, dims, heads):
+    """Pointer and token stride of a projection output [L][B][rows][heads][d], which may be a view of
+    a fused one (any token stride)."""
+    if x is None:
+        return None, 0
+    if not x.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if x.dim() != 5 or tuple(x.shape[:2]) != (dims.L, dims.B) or tuple(x.shape[3:]) != (heads, dims.d):
+        raise ValueError(f"expected [L][B][rows][{heads}][{dims.d}], got {tuple(x.shape)}")
+    s = x.stride(2) if x.shape[2] > 1 else x.stride(1) if x.shape[1] > 1 else x.stride(0) if x.shape[0] > 1 else heads * dims.d
+    want = (x.shape[1] * x.shape[2] * s, x.shape[2] * s, s, dims.d, 1)
+    if any(n > 1 and a != b for n, a, b in zip(x.shape, x.stride(), want)):
+        raise ValueError("tokens must be evenly spaced and a token's heads contiguous")
+    return x.data_ptr(), s
+
+
+def std_qk_norm_rope(d: StdDims, rope: StdRope, q_in, k_in, v_in, rows, n_rows, q_weight, k_weight, eps, pos, q_out,
+                     k_cache, v_cache, cap, length, pos_offset=0, stream=None) -> None:
+    """q_in / k_in / v_in: [L][B][rows][heads][d] tensors or views of a fused projection's output (or None)."""
+    q, qs = _tokens(q_in, d, d.Hq)
+    k, ks = _tokens(k_in, d, d.Hkv)
+    v, vs = _tokens(v_in, d, d.Hkv)
+    _check(lib().std_qk_norm_rope(ctypes.byref(d), ctypes.byref(rope), q, qs, k, ks, v, vs, rows, _ptr(n_rows),
+                                  _ptr(q_weight), _ptr(k_weight), eps, _ptr(pos), _ptr(q_out), _ptr(k_cache),
+                                  _ptr(v_cache), cap, _ptr(length), pos_offset, _stream(stream)))
+
+
+# 4-bit cache: a dict with the std_kv4_cache field names (four tensors and cap), see kv4.Kv4Cache
+
+def _kv4(cache) -> StdKv4Cache:
+    return StdKv4Cache(*[_ptr(cache[f]) for f, _ in StdKv4Cache._fields_])
+
+
+def std_kv4_append(d: StdDims, cache: dict, length, pos_offset, k_new, v_new, n_new, stream=None) -> None:
+    _check(lib().std_kv4_append(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(length), pos_offset, _ptr(k_new),
+                                _ptr(v_new), n_new, _stream(stream)))
+
+
+def std_kv4_quantize(d: StdDims, cache: dict, k_full, v_full, begin, count, max_n, stream=None) -> None:
+    _check(lib().std_kv4_quantize(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(k_full), _ptr(v_full), _ptr(begin),
+                                  _ptr(count), max_n, _stream(stream)))
+
+
+def std_kv4_read(d: StdDims, cache: dict, begin, count, max_n, k_out, v_out, stream=None) -> None:
+    _check(lib().std_kv4_read(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(begin), _ptr(count), max_n, _ptr(k_out),
+                              _ptr(v_out), _stream(stream)))
+
+
+def std_kv4_attn_workspace_size(d: StdDims, q_rows: int, cap: int) -> int:
+    return lib().std_kv4_attn_workspace_size(ctypes.byref(d), q_rows, cap)
+
+
+def std_kv4_attn(d: StdDims, q, q_rows, cache: dict, length, len_offset, o, ws, stream=None) -> None:
+    _check(lib().std_kv4_attn(ctypes.byref(d), _ptr(q), q_rows, ctypes.byref(_kv4(cache)), _ptr(length), len_offset,
+                              _ptr(o), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def std_kv_commit(d: StdDims, k_full, v_full, k_sparse, v_sparse, len_full, len_sparse, n_plus_1, max_n,

@@ -818,6 +818,191 @@ int std_kv_append(const std_dims* dims, void* k_cache, void* v_cache, int64_t ca
   return ok();
 }
 
+// ---------------------------------------------------------------- new tokens' queries and rows
+
+int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_in, int64_t q_stride, const void* k_in,
+                     int64_t k_stride, const void* v_in, int64_t v_stride, int rows, const int32_t* n_rows,
+                     const void* q_weight, const void* k_weight, float eps, const int32_t* pos, void* q_out,
+                     void* k_cache, void* v_cache, int64_t cap, const int32_t* len, int pos_offset,
+                     std_stream_t stream) {
+  STD_NVTX_RANGE();
+  STD_TRY(check_dims(dims));
+  if (!rope) return fail(STD_ERR_INVALID_ARG, "rope is NULL");
+  if (rows < 0 || pos_offset < 0) return fail(STD_ERR_INVALID_ARG, "rows = %d, pos_offset = %d", rows, pos_offset);
+  if (rows == 0) return ok();
+  const int eb = elem_bytes(dims->dtype);
+  if (!q_in && !k_in && !v_in) return fail(STD_ERR_INVALID_ARG, "q_in, k_in and v_in are all NULL");
+  const struct { const void* in; int64_t stride; int heads; void* out; const char *name, *out_name; } parts[] = {
+      {q_in, q_stride, dims->Hq, q_out, "q_in", "q_out"},
+      {k_in, k_stride, dims->Hkv, k_cache, "k_in", "k_cache"},
+      {v_in, v_stride, dims->Hkv, v_cache, "v_in", "v_cache"}};
+  for (const auto& x : parts) {
+    if (!x.in) continue;
+    STD_TRY(check_ptr(x.in, 16, x.name));
+    STD_TRY(check_ptr(x.out, 16, x.out_name));
+    if (x.stride < (int64_t)x.heads * dims->d || (x.stride * eb) % 16)
+      return fail(STD_ERR_INVALID_ARG, "%s: token stride %lld must be at least heads * d = %lld and a multiple of 16 bytes",
+                  x.name, (long long)x.stride, (long long)x.heads * dims->d);
+  }
+  if (q_weight) STD_TRY(check_ptr(q_weight, 16, "q_weight"));
+  if (k_weight) STD_TRY(check_ptr(k_weight, 16, "k_weight"));
+  if ((q_weight || k_weight) && !(eps >= 0.f && eps <= 3.402823466e38f))
+    return fail(STD_ERR_INVALID_ARG, "eps = %g must be finite and >= 0", (double)eps);
+  if (n_rows) STD_TRY(check_ptr(n_rows, 4, "n_rows"));
+  if (pos) STD_TRY(check_ptr(pos, 4, "pos"));
+  if (k_in || v_in || (!pos && rope->rot_dim > 0)) STD_TRY(check_ptr(len, 4, "len"));
+  if (k_in || v_in) {
+    if (cap < 1 || cap > INT32_MAX) return fail(STD_ERR_INVALID_ARG, "cap = %lld", (long long)cap);
+    if ((int64_t)pos_offset + (n_rows ? 0 : rows) > cap) return fail(STD_ERR_CAPACITY, "offset + rows exceed cap");
+  }
+  if (rope->rot_dim < 0 || rope->rot_dim > dims->d) return fail(STD_ERR_INVALID_ARG, "rot_dim = %d", rope->rot_dim);
+  if (rope->rot_dim % (dims->d / 8))
+    return fail(STD_ERR_UNSUPPORTED, "rot_dim = %d must be a multiple of d / 8 = %d", rope->rot_dim, dims->d / 8);
+  if (rope->interleaved != 0 && rope->interleaved != 1)
+    return fail(STD_ERR_INVALID_ARG, "interleaved = %d must be 0 or 1", rope->interleaved);
+  if (rope->rot_dim > 0) STD_TRY(check_ptr(rope->inv_freq, 8, "inv_freq"));
+  if (rope->n_axes < 1 || rope->n_axes > 3) return fail(STD_ERR_INVALID_ARG, "n_axes = %d must be in [1, 3]", rope->n_axes);
+  if (rope->n_axes > 1 && !pos) return fail(STD_ERR_INVALID_ARG, "more than one axis needs positions");
+  int sum = 0;
+  for (int i = 0; i < rope->n_axes; ++i) {
+    if (rope->section[i] < 0 || rope->section[i] > dims->d) return fail(STD_ERR_INVALID_ARG, "section[%d] = %d", i, rope->section[i]);
+    sum += rope->section[i];
+  }
+  if (sum != rope->rot_dim / 2)
+    return fail(STD_ERR_INVALID_ARG, "the sections hold %d pairs, rot_dim / 2 = %d", sum, rope->rot_dim / 2);
+  // (the kernel numbers its CTAs in 31 bits: at most one for 16 heads of a token)
+  if ((int64_t)dims->L * dims->B * (rows / 4 + 1) > (1 << 30)) return fail(STD_ERR_INVALID_ARG, "too many tokens");
+  int *err, sms;
+  STD_TRY(device_state(&err, &sms));
+  stdb::RopeArgs a{};
+  a.q_in = q_in; a.k_in = k_in; a.v_in = v_in; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.rows = rows; a.n_rows = n_rows; a.q_w = q_weight; a.k_w = k_weight; a.eps = eps; a.pos = pos;
+  a.inv_freq = rope->inv_freq; a.rot_dim = rope->rot_dim; a.interleaved = rope->interleaved;
+  a.sec_end[0] = rope->section[0];
+  a.sec_end[1] = rope->n_axes > 1 ? rope->section[0] + rope->section[1] : rope->section[0];
+  a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache; a.cap = cap; a.len = len; a.pos_offset = pos_offset;
+  a.L = dims->L; a.B = dims->B; a.Hq = dims->Hq; a.Hkv = dims->Hkv; a.d = dims->d; a.dtype = dims->dtype; a.err = err;
+  cudaError_t e = stdb::launch_qk_norm_rope(a, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------- 4-bit cache
+
+namespace {
+
+int check_kv4(const std_dims* dims, const std_kv4_cache* c) {
+  STD_TRY(check_dims(dims));
+  if (!c) return fail(STD_ERR_INVALID_ARG, "cache is NULL");
+  if (dims->d != 64 && dims->d != 128) return fail(STD_ERR_UNSUPPORTED, "4-bit cache: head dim %d (supported: 64, 128)", dims->d);
+  STD_TRY(check_ptr(c->k_codes, 16, "k_codes"));
+  STD_TRY(check_ptr(c->k_scales, 16, "k_scales"));
+  STD_TRY(check_ptr(c->v_codes, 16, "v_codes"));
+  STD_TRY(check_ptr(c->v_scales, 16, "v_scales"));
+  if (c->cap < 16 || c->cap > INT32_MAX || c->cap % 16)
+    return fail(STD_ERR_INVALID_ARG, "cap = %lld must be a positive multiple of 16", (long long)c->cap);
+  return STD_OK;
+}
+
+int run_kv4(const std_dims* dims, const std_kv4_cache* c, const void* k, const void* v, int64_t rows_cap, int at_pos,
+            const int32_t* begin, const int32_t* count, int max_n, int pos_offset, bool read, cudaStream_t stream) {
+  if (max_n < 0 || pos_offset < 0) return fail(STD_ERR_INVALID_ARG, "rows = %d, pos_offset = %d", max_n, pos_offset);
+  if (max_n == 0) return ok();
+  STD_TRY(check_ptr(k, 16, read ? "k_out" : "k rows"));
+  STD_TRY(check_ptr(v, 16, read ? "v_out" : "v rows"));
+  if (begin) STD_TRY(check_ptr(begin, 4, "begin"));
+  if (count) STD_TRY(check_ptr(count, 4, "count"));
+  // with counts on the device max_n is a bound, which may pass the capacity
+  if (!count && (int64_t)max_n + pos_offset > c->cap) return fail(STD_ERR_CAPACITY, "offset + rows exceed cap");
+  if (!count && at_pos && max_n > rows_cap) return fail(STD_ERR_CAPACITY, "rows exceed cap_full");
+  if (2 * (int64_t)probs_of(dims) * (max_n / 64 + 1) > INT32_MAX) return fail(STD_ERR_INVALID_ARG, "too many rows");
+  int* err;
+  STD_TRY(device_state(&err, nullptr));
+  stdb::Kv4Args a{};
+  a.k = k; a.v = v; a.rows_cap = rows_cap; a.at_pos = at_pos;
+  a.k_codes = c->k_codes; a.k_scales = c->k_scales; a.v_codes = c->v_codes; a.v_scales = c->v_scales; a.cap = c->cap;
+  a.begin = begin; a.count = count; a.max_n = max_n; a.pos_offset = pos_offset;
+  a.L = dims->L; a.B = dims->B; a.Hkv = dims->Hkv; a.d = dims->d; a.dtype = dims->dtype; a.err = err;
+  cudaError_t e = stdb::launch_kv4(a, read, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit cache launch");
+  return ok();
+}
+
+int plan_kv4(const std_dims* dims, int q_rows, int64_t cap, stdb::Kv4AttnArgs* a) {
+  STD_TRY(check_dims(dims));
+  if (dims->d != 64 && dims->d != 128) return fail(STD_ERR_UNSUPPORTED, "4-bit cache: head dim %d (supported: 64, 128)", dims->d);
+  if (dims->B > stdb::kKv4AttnMaxB)
+    return fail(STD_ERR_UNSUPPORTED, "4-bit attention: %d sequences (at most %d)", dims->B, stdb::kKv4AttnMaxB);
+  if (q_rows < 1 || q_rows > 32) return fail(STD_ERR_INVALID_ARG, "q_rows = %d must be in [1, 32]", q_rows);
+  if (cap < 16 || cap > INT32_MAX || cap % 16)
+    return fail(STD_ERR_INVALID_ARG, "cap = %lld must be a positive multiple of 16", (long long)cap);
+  *a = stdb::Kv4AttnArgs{};
+  a->L = dims->L; a->B = dims->B; a->Hq = dims->Hq; a->Hkv = dims->Hkv; a->G = dims->Hq / dims->Hkv; a->nq = q_rows;
+  a->rows = a->G * q_rows; a->d = dims->d; a->dtype = dims->dtype; a->cap = cap;
+  if (a->rows > 128) return fail(STD_ERR_UNSUPPORTED, "G * query rows = %d exceeds 128", a->rows);
+  if ((int64_t)probs_of(dims) * 128 > INT32_MAX || (int64_t)probs_of(dims) * 16 * ((cap + 127) / 128) > INT32_MAX)
+    return fail(STD_ERR_UNSUPPORTED, "too many (layer, sequence, head) problems for this capacity");
+  int sms;
+  STD_TRY(device_state(nullptr, &sms));
+  stdb::plan_kv4_attn(a, sms);
+  return STD_OK;
+}
+
+}  // namespace
+
+int std_kv4_append(const std_dims* dims, const std_kv4_cache* cache, const int32_t* len, int pos_offset,
+                   const void* k_new, const void* v_new, int n_new, std_stream_t stream) {
+  STD_NVTX_RANGE();
+  STD_TRY(check_kv4(dims, cache));
+  STD_TRY(check_ptr(len, 4, "len"));
+  return run_kv4(dims, cache, k_new, v_new, n_new, 0, len, nullptr, n_new, pos_offset, false, stream);
+}
+
+int std_kv4_quantize(const std_dims* dims, const std_kv4_cache* cache, const void* k_full, const void* v_full,
+                     const int32_t* begin, const int32_t* count, int max_n, std_stream_t stream) {
+  STD_NVTX_RANGE();
+  STD_TRY(check_kv4(dims, cache));
+  return run_kv4(dims, cache, k_full, v_full, dims->cap_full, 1, begin, count, max_n, 0, false, stream);
+}
+
+int std_kv4_read(const std_dims* dims, const std_kv4_cache* cache, const int32_t* begin, const int32_t* count,
+                 int max_n, void* k_out, void* v_out, std_stream_t stream) {
+  STD_NVTX_RANGE();
+  STD_TRY(check_kv4(dims, cache));
+  return run_kv4(dims, cache, k_out, v_out, max_n, 0, begin, count, max_n, 0, true, stream);
+}
+
+size_t std_kv4_attn_workspace_size(const std_dims* dims, int q_rows, int64_t cap) {
+  stdb::Kv4AttnArgs a;
+  if (plan_kv4(dims, q_rows, cap, &a)) return 0;
+  return (size_t)a.ws_floats * sizeof(float);
+}
+
+int std_kv4_attn(const std_dims* dims, const void* q, int q_rows, const std_kv4_cache* cache, const int32_t* len,
+                 int len_offset, void* o, void* ws, size_t ws_bytes, std_stream_t stream) {
+  STD_NVTX_RANGE();
+  STD_TRY(check_kv4(dims, cache));
+  STD_TRY(check_ptr(q, 16, "q"));
+  STD_TRY(check_ptr(len, 4, "len"));
+  STD_TRY(check_ptr(o, 16, "o"));
+  if (len_offset < 0) return fail(STD_ERR_INVALID_ARG, "len_offset = %d must be >= 0", len_offset);
+  stdb::Kv4AttnArgs a;
+  STD_TRY(plan_kv4(dims, q_rows, cache->cap, &a));
+  if ((int64_t)len_offset + q_rows - 1 > cache->cap) return fail(STD_ERR_CAPACITY, "len_offset + q_rows exceeds cap");
+  const size_t need = (size_t)a.ws_floats * sizeof(float);
+  if (!ws || ws_bytes < need)
+    return fail(STD_ERR_WORKSPACE, "attention workspace: need %zu bytes, got %zu", need, ws ? ws_bytes : 0);
+  STD_TRY(check_ptr(ws, 16, "ws"));
+  int* err;
+  STD_TRY(device_state(&err, nullptr));
+  a.q = q; a.o = o; a.len = len; a.len_off = len_offset; a.ws = static_cast<float*>(ws); a.err = err;
+  a.k_codes = static_cast<const uint8_t*>(cache->k_codes); a.k_scales = static_cast<const uint8_t*>(cache->k_scales);
+  a.v_codes = static_cast<const uint8_t*>(cache->v_codes); a.v_scales = static_cast<const uint8_t*>(cache->v_scales);
+  cudaError_t e = stdb::launch_kv4_attn(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
+  return ok();
+}
+
 int std_kv_commit(const std_dims* dims, void* k_full, void* v_full, void* k_sparse, void* v_sparse,
                   int32_t* len_full, int32_t* len_sparse, const int32_t* n_plus_1, int max_n,
                   std_stream_t stream) {

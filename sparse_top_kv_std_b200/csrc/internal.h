@@ -209,6 +209,75 @@ cudaError_t launch_commit(void* k_full, void* v_full, void* k_sp, void* v_sp, in
 cudaError_t launch_merge_partials(int64_t rows, int d, int n_parts, const float* o_parts, const float* ml_parts,
                                   float* o, int sms, cudaStream_t s);
 
+// Norm, rotation and append of new tokens' queries, keys and values (rope.cu).
+struct RopeArgs {
+  const void* q_in;  // [L][B][rows][Hq][d], neighbouring tokens q_stride elements apart; NULL: none
+  const void* k_in;
+  const void* v_in;
+  int64_t q_stride, k_stride, v_stride;
+  int rows;
+  const int32_t* n_rows;  // [B] or NULL: every sequence has `rows`
+  const void* q_w;        // [L][d] or NULL: no norm
+  const void* k_w;
+  float eps;
+  const int32_t* pos;  // [axes][B][rows] or NULL: the cache position
+  const double* inv_freq;
+  int rot_dim, interleaved;
+  int sec_end[2];  // pairs below sec_end[0] turn with axis 0, below sec_end[1] with axis 1
+  void* q_out;     // [L][B][Hq][rows][d]
+  void* k_cache;   // [L][B][Hkv][cap][d]
+  void* v_cache;
+  int64_t cap;
+  const int32_t* len;
+  int pos_offset;
+  int L, B, Hq, Hkv, d, dtype;
+  int* err;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int sms, cudaStream_t s);
+
+// Rows into (read = false) or out of a 4-bit cache (kv4.cu): r < count[b] of every sequence, cache
+// rows begin[b] + pos_offset + r, other side's rows r (at_pos: the cache rows) of buffers of
+// rows_cap rows for each (layer, sequence, KV head).
+struct Kv4Args {
+  const void* k;
+  const void* v;
+  int64_t rows_cap;
+  int at_pos;
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int64_t cap;
+  const int32_t* begin;
+  const int32_t* count;
+  int max_n, pos_offset;
+  int L, B, Hkv, d, dtype;
+  int* err;
+};
+cudaError_t launch_kv4(const Kv4Args& a, bool read, cudaStream_t s);
+
+// Decode attention over a 4-bit cache (kv4_attn.cu): query row r = g * nq + i of a KV head
+// attends keys j < len[b] + len_off + i.
+constexpr int kKv4AttnMaxB = 1024;
+struct Kv4AttnArgs {
+  const void* q;
+  void* o;
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_codes;
+  const uint8_t* v_scales;
+  int64_t cap;
+  const int32_t* len;
+  int len_off;
+  int L, B, Hq, Hkv, G, nq, rows, d, dtype;
+  int row_blocks, ctas;  // set by plan_kv4_attn, with the workspace it needs
+  int64_t ws_floats;
+  float* ws;
+  int* err;
+};
+void plan_kv4_attn(Kv4AttnArgs* a, int sms);
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
+
 cudaError_t launch_accept(int B, int gamma, const int32_t* draft, const int32_t* dense,
                           int32_t* n_plus_1, int32_t* accepted, cudaStream_t s);
 

@@ -1,0 +1,802 @@
+// Decode attention over a 4-bit K/V cache (format: kv4.cuh), for one query position (a draft
+// step) up to gamma + 1 causal ones.
+//
+//   K_jc = mk_jg + sk_jg a_jc,  V_jc = mv_jg + sv_jg b_jc       codes a, b in 0..15, group g of channel c
+//   x_rj = sum_g sk_jg (q_r . (a_j - 8))_g + (mk_jg + 8 sk_jg) (sum q_r)_g          scaled by log2(e) / sqrt(d)
+//   o_rc = [ sum_j (p_rj sv_jg) (b_jc - 8) + sum_j p_rj (mv_jg + 8 sv_jg) ] / sum_j p_rj,   p = 2^(x - M_r)
+//
+// so the scales never touch the codes: K's multiply the two partial dot products of a key, V's
+// multiply the weights, and what the tensor cores see of a code is the small integer c - 8,
+// exact in fp16.  (Codes are centred because sum p b would otherwise grow without bound while
+// the answer stays near the mean: at 140,000 keys the fp32 accumulator would lose it.)
+//
+// A byte of the cache feeds 2 G x rows multiply-adds, and a key's codes have to be widened
+// before any of them: at d = 128 a (row, head) is 144 bytes, against 512 in bf16, and its 256
+// codes cost about two instructions each, which leaves a third of the issue slots at full HBM
+// rate.  So the widened codes go straight from registers into mma.sync (m16n8k16: 16 keys or 16
+// channels by 8 query rows), with no shared-memory round trip: K is the A operand of S^T = K q^T,
+// V^T the A operand of O^T = V^T P^T, and one movmatrix turns S^T's accumulator layout into
+// P^T's operand layout.  A 5th-generation MMA would need the operand written to shared or
+// tensor memory first, for 8 of its 128 columns.
+//
+// The 128-key tiles of all (layer, sequence, KV head, row block) units form one sequence that
+// the CTAs split evenly; bulk copies stream the tiles through a shared-memory ring, and each of
+// eight warps takes 16 keys of every tile with a softmax state of its own.  The states merge once for each unit a CTA touches; units that several CTAs touch merge
+// in a second kernel.
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "tc100.cuh"
+
+#include <cuda_fp16.h>
+
+namespace stdb {
+namespace {
+
+constexpr int kTile = 128;               // keys of a tile
+constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLimit = 32768.f;        // largest weight x scale that goes to fp16
+constexpr float kSmall = 9.094947e-13f;  // 2^-40: scales below it count as this much, so that p stays below 2^55
+constexpr float kHeadroom = 8.f;         // a new reference puts the largest one at 2^8
+
+// ---------------------------------------------------------------- shared memory
+template <int D, int NT>
+struct Layout {
+  static constexpr int CW = D / 2;                      // code bytes of a row
+  static constexpr int SW = D / kKv4Group * 4;          // scale bytes of a row
+  static constexpr int STAGE = 2 * kTile * (CW + SW);   // K codes, V codes, K scales, V scales
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int OSTR = D + 4;                    // row stride of the merge buffer, floats
+  static constexpr int MERGE = kWarps * ROWS * OSTR * 4;
+  static constexpr int BUDGET = NT == 1 ? 108 * 1024 : 216 * 1024;
+  static constexpr int FIT = (BUDGET - MERGE) / STAGE;
+  static constexpr int STAGES = FIT < 16 ? FIT : 16;
+  static constexpr int BYTES = STAGES * STAGE + MERGE;
+};
+
+constexpr int kMaxStages = 16;
+struct Ctl {
+  uint64_t full[kMaxStages];
+  int done[kMaxStages];  // warps that have read the stage's tile
+  // the next tile to fetch (touched only by the thread that fetches it)
+  int fills, next, left, first, keys;
+  int64_t row0;  // cache row of the unit's row 0
+  float m[kWarps][16], l[kWarps][16];
+  int cum[kKv4AttnMaxB + 1];  // tiles of the sequences before b
+  volatile int abort;
+};
+
+// ---------------------------------------------------------------- work split
+// Units are numbered (layer, sequence, KV head, row block); sequence b has tiles(b) tiles in each.
+struct Unit {
+  int l, b, h, rb, tile0, tiles;  // tile0: the tile within the unit; tiles: the unit's
+};
+
+__device__ __forceinline__ int seq_tiles(const Kv4AttnArgs& a, int b, int* keys) {
+  const int64_t n0 = (int64_t)a.len[b] + a.len_off, n = n0 + a.nq - 1;
+  if (a.len[b] < 0 || n > a.cap) return -1;
+  *keys = (int)n;
+  return n < 1 ? 1 : (int)((n + kTile - 1) / kTile);
+}
+
+// Prefix sums of the sequences' tiles by one warp; an invalid sequence has none.
+__device__ __forceinline__ void scan_tiles(const Kv4AttnArgs& a, int* cum, int lane, bool flag) {
+  int run = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int keys, t = 0;
+    if (b < a.B) {
+      t = seq_tiles(a, b, &keys);
+      if (t < 0) {
+        if (flag) flag_error(a.err, STD_DEVERR_LENGTH);
+        t = 0;
+      }
+    }
+    int s = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (b < a.B) cum[b + 1] = run + s;
+    run += __shfl_sync(0xffffffffu, s, 31);
+  }
+  if (lane == 0) cum[0] = 0;
+}
+
+__device__ __forceinline__ Unit locate(const Kv4AttnArgs& a, const int* cum, int t) {
+  Unit u;
+  const int per_tile = a.Hkv * a.row_blocks;
+  const int tl = cum[a.B] * per_tile;  // tiles of a layer
+  u.l = t / tl;
+  int r = t - u.l * tl;
+  int lo = 0, hi = a.B;  // the last b with cum[b] * per_tile <= r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] * per_tile <= r) lo = mid; else hi = mid;
+  }
+  u.b = lo;
+  r -= cum[lo] * per_tile;
+  u.tiles = cum[lo + 1] - cum[lo];
+  const int hr = r / u.tiles;
+  u.tile0 = r - hr * u.tiles;
+  u.h = hr / a.row_blocks;
+  u.rb = hr - u.h * a.row_blocks;
+  return u;
+}
+
+__device__ __forceinline__ int cta_begin(int tiles, int ctas, int c) { return (int)((int64_t)tiles * c / ctas); }
+
+// ---------------------------------------------------------------- instructions
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // 16-bit elements, rows over lane / 4
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// Codes to fp16: 0x6400 is 1024, whose last ten bits hold a code at bit 0 (1024 + c) or at
+// bit 4 (1024 + 16 c); one exact subtraction or fused multiply-add leaves c - 8.
+__device__ __forceinline__ uint32_t widen0(uint32_t w) {  // bits 0-3 and 16-19
+  return as_u32(__hsub2(as_h2((w & 0x000f000fu) | 0x64006400u), __float2half2_rn(1032.f)));
+}
+__device__ __forceinline__ uint32_t widen4(uint32_t w) {  // bits 4-7 and 20-23
+  return as_u32(__hfma2(as_h2((w & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ float max_of(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float column_sum(float v) {  // over the eight lanes of one accumulator column
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+
+// ---------------------------------------------------------------- a warp's state for one unit
+// Lane = 4 g + t.  Query rows are the n index of the matrix instructions: as an operand a lane
+// holds row g of each 8-row block, in an accumulator rows 2 t and 2 t + 1.  Accumulator row
+// m of S^T is key kappa(m) of the warp's 16: for m < 8 even m are keys m / 2 and odd m
+// keys 4 + (m / 2 ^ 1), and likewise 8 higher.  So the four V rows that lane t multiplies
+// (operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9) are t, 4 + (t ^ 1), 8 + t and 12 + (t ^ 1): four
+// neighbouring rows for the quad, and the K rows of neighbouring g lie in different banks.
+template <int D, int NT, bool F32>
+struct State {
+  static constexpr int KS = D / 16;          // k-steps of S^T
+  static constexpr int GR = D / kKv4Group;   // groups
+  static constexpr int MT = D / 16;          // 16-channel tiles of O^T
+  uint32_t qh[NT][KS][2];                    // q, scaled by a power of two, as the B operand
+  uint32_t ql[F32 ? NT : 1][F32 ? KS : 1][2];  // its remainder below fp16 (fp32 queries)
+  float rs[NT][2];                           // x = rs * (K . scaled q)
+  float qsum[NT][GR][2];                     // sum of the scaled q over a group
+  int lim[NT][2];                            // keys the row attends
+  float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
+  float o[NT][MT][4];                        // sum (p sv) (b - 8)
+};
+
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, int n0,
+                                             int lane) {
+  using S = State<D, NT, F32>;
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int WPL = D / 32;  // words of a row that lane t multiplies
+  const float scale = kLog2e * rsqrtf((float)D);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = u.rb * 8 * NT + nt * 8 + g;
+    float x[WPL][8];
+    float top = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPL; ++w) {
+      const int ch = kv4_word_channel<D>(WPL * t + w);
+      if (r < a.rows) {
+        const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + ch;
+        if constexpr (F32) {
+          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+          const float4 v0 = p[0], v1 = p[1];
+          x[w][0] = v0.x; x[w][1] = v0.y; x[w][2] = v0.z; x[w][3] = v0.w;
+          x[w][4] = v1.x; x[w][5] = v1.y; x[w][6] = v1.z; x[w][7] = v1.w;
+        } else {
+          const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+          x[w][0] = lo_bf16(v.x); x[w][1] = hi_bf16(v.x); x[w][2] = lo_bf16(v.y); x[w][3] = hi_bf16(v.y);
+          x[w][4] = lo_bf16(v.z); x[w][5] = hi_bf16(v.z); x[w][6] = lo_bf16(v.w); x[w][7] = hi_bf16(v.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[w][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[w][i]));
+    }
+    top = quad_max(top);
+    // scale the row by a power of two that puts its largest entry in [2^14, 2^15): exact, and
+    // entries down to 2^-28 of it keep all their bits in fp16
+    int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+    ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;
+    const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+    float sum[S::GR];
+#pragma unroll
+    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPL; ++w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[w][i] *= mul;
+        sum[S::GR == 2 ? (w & 1) : 0] += x[w][i];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // channels 2 k + e and 2 k + e + 4 of the word: one register pair
+          const __half2 hv = __floats2half2_rn(x[w][2 * k + e], x[w][2 * k + e + 4]);
+          st.qh[nt][2 * w + k][e] = as_u32(hv);
+          if constexpr (F32) {
+            const float2 f = __half22float2(hv);
+            st.ql[nt][2 * w + k][e] =
+                as_u32(__floats2half2_rn(x[w][2 * k + e] - f.x, x[w][2 * k + e + 4] - f.y));
+          }
+        }
+    }
+    const float back = scale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+#pragma unroll
+    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int from = 4 * (2 * t + e);  // a lane that holds row 2 t + e
+      st.rs[nt][e] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr) st.qsum[nt][gr][e] = __shfl_sync(0xffffffffu, sum[gr], from);
+      const int row = u.rb * 8 * NT + nt * 8 + 2 * t + e;
+      st.lim[nt][e] = n0 + (row < a.rows ? row % a.nq : 0);
+      st.M[nt][e] = -INFINITY;
+      st.l[nt][e] = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr) st.pm[nt][gr][e] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.o[nt][mt][i] = 0.f;
+  }
+}
+
+// 16 keys: rows [row0, row0 + 16) of the tile at shared addresses kc / vc / ks / vs, key0 = the
+// first one's position.  MASK: some of them may lie past a row's limit (or past the cache,
+// where the shared memory holds stale bytes: codes are finite whatever they are, scales are not).
+template <int D, int NT, bool F32, bool MASK>
+__device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uint32_t vc, uint32_t ks, uint32_t vs,
+                                         int row0, int key0, int lane) {
+  using S = State<D, NT, F32>;
+  using Lay = Layout<D, NT>;
+  constexpr int GR = S::GR, WPL = D / 32;
+  const int g = lane >> 2, t = lane & 3;
+  const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);  // key of accumulator row g; row g + 8 is 8 higher
+
+  // S^T: two partial products, one for each group
+  float acc[NT][GR][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][gr][i] = 0.f;
+  uint32_t wa[WPL], wb[WPL];
+  {
+    const uint32_t ra = kc + (row0 + kap) * Lay::CW + t * (WPL * 4), rb = ra + 8 * Lay::CW;
+    if constexpr (WPL == 4) {
+      const uint4 x = lds128(ra), y = lds128(rb);
+      wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
+      wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+    } else {
+      const uint2 x = lds64(ra), y = lds64(rb);
+      wa[0] = x.x; wa[1] = x.y;
+      wb[0] = y.x; wb[1] = y.y;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < WPL; ++w) {
+    const int gr = GR == 2 ? (w & 1) : 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x = k ? wa[w] >> 8 : wa[w], y = k ? wb[w] >> 8 : wb[w];
+      const uint32_t a0 = widen0(x), a1 = widen0(y), a2 = widen4(x), a3 = widen4(y);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
+        if constexpr (F32) mma_f16(acc[nt][gr], a0, a1, a2, a3, st.ql[nt][2 * w + k][0], st.ql[nt][2 * w + k][1]);
+      }
+    }
+  }
+
+  // scales of keys kap and kap + 8
+  float sk[2][GR], mk[2][GR], sv[2][GR], mv[2][GR], smax[2];
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    const uint32_t at = (row0 + kap + 8 * hf) * Lay::SW;
+    uint32_t uk[GR], uv[GR];
+    if constexpr (GR == 2) {
+      const uint2 x = lds64(ks + at), y = lds64(vs + at);
+      uk[0] = x.x; uk[1] = x.y; uv[0] = y.x; uv[1] = y.y;
+    } else {
+      uk[0] = lds32(ks + at);
+      uv[0] = lds32(vs + at);
+    }
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr) {
+      sk[hf][gr] = lo_bf16(uk[gr]);
+      mk[hf][gr] = fmaf(8.f, sk[hf][gr], hi_bf16(uk[gr]));
+      sv[hf][gr] = lo_bf16(uv[gr]);
+      mv[hf][gr] = fmaf(8.f, sv[hf][gr], hi_bf16(uv[gr]));
+    }
+    smax[hf] = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
+  }
+
+  // logits (log2 domain); element i of an accumulator: key half i / 2, row 2 t + i % 2
+  float x[NT][4];
+  bool seen[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int hf = i >> 1, e = i & 1;
+      float y = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) {
+        y = fmaf(sk[hf][gr], acc[nt][gr][i], y);
+        y = fmaf(mk[hf][gr], st.qsum[nt][gr][e], y);
+      }
+      x[nt][i] = y * st.rs[nt][e];
+      seen[nt][i] = !MASK || key0 + kap + 8 * hf < st.lim[nt][e];
+    }
+
+  // weights against the running reference M; p sv has to fit fp16, and where it does not (or
+  // no reference is set yet) the references of this warp's rows move up first
+  float p[NT][4];
+  float big = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[nt][i] = ex2(x[nt][i] - st.M[nt][i & 1]);
+      if (seen[nt][i] && !(p[nt][i] * smax[i >> 1] <= kLimit)) big = 1.f;  // (a NaN counts)
+    }
+  if (__any_sync(0xffffffffu, big != 0.f)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float z = -INFINITY;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          if (seen[nt][2 * hf + e])
+            z = fmaxf(z, x[nt][2 * hf + e] + __log2f(smax[hf]));
+        z = column_max(z);
+        if (z - st.M[nt][e] > 14.9f) {
+          const float m1 = z - kHeadroom;
+          const float f = ex2(st.M[nt][e] - m1);
+          st.M[nt][e] = m1;
+          st.l[nt][e] *= f;
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) st.pm[nt][gr][e] *= f;
+#pragma unroll
+          for (int mt = 0; mt < S::MT; ++mt) {
+            st.o[nt][mt][e] *= f;
+            st.o[nt][mt][2 + e] *= f;
+          }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) p[nt][2 * hf + e] = ex2(x[nt][2 * hf + e] - st.M[nt][e]);
+      }
+  }
+
+  // P^T operands: rows of a key pack side by side, and an 8 x 8 transposition puts keys there
+  uint32_t ph[NT][GR][2], pl[F32 ? NT : 1][F32 ? GR : 1][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (MASK && !seen[nt][i]) p[nt][i] = 0.f;
+      st.l[nt][i & 1] += p[nt][i];
+    }
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float w0 = p[nt][2 * hf] * sv[hf][gr], w1 = p[nt][2 * hf + 1] * sv[hf][gr];
+        float c0 = p[nt][2 * hf] * mv[hf][gr], c1 = p[nt][2 * hf + 1] * mv[hf][gr];
+        if constexpr (MASK) {  // a scale past the limit may be anything
+          if (!seen[nt][2 * hf]) w0 = c0 = 0.f;
+          if (!seen[nt][2 * hf + 1]) w1 = c1 = 0.f;
+        }
+        st.pm[nt][gr][0] += c0;
+        st.pm[nt][gr][1] += c1;
+        const __half2 hv = __floats2half2_rn(w0, w1);
+        ph[nt][gr][hf] = transpose8x8(as_u32(hv));
+        if constexpr (F32) {
+          const float2 f = __half22float2(hv);
+          pl[nt][gr][hf] = transpose8x8(as_u32(__floats2half2_rn(w0 - f.x, w1 - f.y)));
+        }
+      }
+  }
+
+  // O^T += V^T P^T: lane t's keys, two words (d = 128: one of each group) of 8 channels at 8 g
+  uint32_t v[4][GR];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = 4 * i + ((i & 1) ? (t ^ 1) : t);
+    const uint32_t at = vc + (row0 + key) * Lay::CW + g * (4 * GR);
+    if constexpr (GR == 2) {
+      const uint2 y = lds64(at);
+      v[i][0] = y.x; v[i][1] = y.y;
+    } else {
+      v[i][0] = lds32(at);
+    }
+  }
+#pragma unroll
+  for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+    for (int hw = 0; hw < 2; ++hw) {  // low and high halves of the words: channels 0-3 and 4-7
+      const uint32_t y01 = __byte_perm(v[0][gr], v[1][gr], hw ? 0x7632 : 0x5410);
+      const uint32_t y23 = __byte_perm(v[2][gr], v[3][gr], hw ? 0x7632 : 0x5410);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t b01 = k ? y01 >> 8 : y01, b23 = k ? y23 >> 8 : y23;
+        const uint32_t a0 = widen0(b01), a1 = widen4(b01), a2 = widen0(b23), a3 = widen4(b23);
+        const int mt = gr * 4 + hw * 2 + k;  // rows g: channel 8 g + 2 (2 hw + k), rows g + 8: the next one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(st.o[nt][mt], a0, a1, a2, a3, ph[nt][gr][0], ph[nt][gr][1]);
+          if constexpr (F32) mma_f16(st.o[nt][mt], a0, a1, a2, a3, pl[nt][gr][0], pl[nt][gr][1]);
+        }
+      }
+    }
+}
+
+__device__ __forceinline__ void compute_sync() { __syncthreads(); }
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = v;
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  }
+}
+
+// Partials of one slot: [8 NT][D] unnormalised sums, then [8 NT][2] (reference, sum of weights).
+template <int D>
+__host__ __device__ constexpr int64_t slot_floats(int rows) { return (int64_t)rows * (D + 2); }
+
+// Merge the warps' states of one unit and write the output (`whole`) or the partial slot.
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, Ctl* ctl,
+                                            float* buf, bool whole, float* slot, int warp, int lane) {
+  using S = State<D, NT, F32>;
+  using Lay = Layout<D, NT>;
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      st.l[nt][e] = column_sum(st.l[nt][e]);
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr) {
+        const float c = column_sum(st.pm[nt][gr][e]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          st.o[nt][gr * 4 + i][e] += c;
+          st.o[nt][gr * 4 + i][2 + e] += c;
+        }
+      }
+      if (g == 0) {
+        ctl->m[warp][nt * 8 + 2 * t + e] = st.M[nt][e];
+        ctl->l[warp][nt * 8 + 2 * t + e] = st.l[nt][e];
+      }
+    }
+  compute_sync();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int n = nt * 8 + 2 * t + e;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ctl->m[w][n]);
+      const float f = st.M[nt][e] == -INFINITY ? 0.f : ex2(st.M[nt][e] - top);
+      float* row = buf + (warp * Lay::ROWS + n) * Lay::OSTR;
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float4*>(row + gr * 64 + 8 * g + 4 * i) =
+              make_float4(st.o[nt][gr * 4 + 2 * i][e] * f, st.o[nt][gr * 4 + 2 * i][2 + e] * f,
+                          st.o[nt][gr * 4 + 2 * i + 1][e] * f, st.o[nt][gr * 4 + 2 * i + 1][2 + e] * f);
+    }
+  compute_sync();
+  for (int i = warp * 32 + lane; i < Lay::ROWS * (D / 4); i += kWarps * 32) {
+    const int n = i / (D / 4), c = (i - n * (D / 4)) * 4;
+    const int r = u.rb * Lay::ROWS + n;
+    if (r >= a.rows) break;
+    float top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ctl->m[w][n]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float m = ctl->m[w][n];
+      l += m == -INFINITY ? 0.f : ctl->l[w][n] * ex2(m - top);
+      const float4 v = *reinterpret_cast<const float4*>(buf + (w * Lay::ROWS + n) * Lay::OSTR + c);
+      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+    }
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that attends no key: zeros
+      const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + c;
+      store4(static_cast<T*>(a.o) + at, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(slot + n * D + c) = sum;
+      if (c == 0) *reinterpret_cast<float2*>(slot + Lay::ROWS * D + 2 * n) = make_float2(top, l);
+    }
+  }
+  compute_sync();  // the buffers are free for the next unit
+}
+
+// Fetch the next tile of this CTA's range into its stage (one thread at a time, in order).
+template <int D, int NT>
+__device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Ctl* ctl, uint32_t ring, int end) {
+  using Lay = Layout<D, NT>;
+  while (ctl->left == 0) {
+    const int t = ctl->next;
+    if (t >= end) return;
+    const Unit u = locate(a, ctl->cum, t);
+    const int n = min(u.tiles - u.tile0, end - t);
+    int keys = 0;
+    seq_tiles(a, u.b, &keys);
+    ctl->next = t + n;
+    ctl->left = keys > u.tile0 * kTile ? n : 0;  // (a sequence without keys has nothing to fetch)
+    ctl->first = u.tile0 * kTile;
+    ctl->keys = keys;
+    ctl->row0 = (((int64_t)u.l * a.B + u.b) * a.Hkv + u.h) * a.cap;
+  }
+  const int first = ctl->first, stage = ctl->fills % Lay::STAGES;
+  // whole 16-row blocks: the capacity is a multiple of 16, so they end inside the cache
+  const uint32_t rows = min(kTile, (ctl->keys - first + 15) & ~15);
+  const int64_t row = ctl->row0 + first;
+  const uint32_t dst = ring + stage * Lay::STAGE;
+  uint64_t* bar = &ctl->full[stage];
+  tc::mbar_expect_tx(bar, 2 * rows * (Lay::CW + Lay::SW));
+  bulk_load(dst, a.k_codes + row * Lay::CW, rows * Lay::CW, bar);
+  bulk_load(dst + 2 * kTile * Lay::CW, a.k_scales + row * Lay::SW, rows * Lay::SW, bar);
+  bulk_load(dst + kTile * Lay::CW, a.v_codes + row * Lay::CW, rows * Lay::CW, bar);
+  bulk_load(dst + kTile * (2 * Lay::CW + Lay::SW), a.v_scales + row * Lay::SW, rows * Lay::SW, bar);
+  ctl->fills += 1;
+  ctl->first = first + kTile;
+  ctl->left -= 1;
+}
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
+  using Lay = Layout<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Ctl ctl;
+  constexpr int STAGES = Lay::STAGES;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(&ctl.full[s], 1);
+      ctl.done[s] = 0;
+    }
+    ctl.abort = 0;
+    ctl.fills = ctl.left = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
+  pdl_trigger();
+  if (warp == 0) scan_tiles(a, ctl.cum, lane, blockIdx.x == 0);
+  __syncthreads();
+  const int total = ctl.cum[a.B] * a.Hkv * a.row_blocks * a.L;
+  if (total == 0) return;
+  const int begin = cta_begin(total, gridDim.x, blockIdx.x), end = cta_begin(total, gridDim.x, blockIdx.x + 1);
+  const uint32_t ring = smem_u32(smem);
+  if (tid == 0) {
+    ctl.next = begin;
+    for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT>(a, &ctl, ring, end);
+  }
+  int stage = 0;
+  uint32_t phase = 0;
+  State<D, NT, F32> st;
+  bool ok = true;
+  for (int t = begin; t < end;) {
+    const Unit u = locate(a, ctl.cum, t);
+    const int n = min(u.tiles - u.tile0, end - t);
+    int keys = 0;
+    seq_tiles(a, u.b, &keys);
+    const int n0 = keys - a.nq + 1;  // keys that query position 0 attends
+    load_queries<D, NT, F32>(st, a, u, n0, lane);
+    for (int i = 0; i < n; ++i) {
+      const int first = (u.tile0 + i) * kTile;
+      if (first >= keys) break;
+      ok = ok && tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err);
+      if (ok) {
+        const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
+                       vs = ks + kTile * Lay::SW;
+        const int key0 = first + 16 * warp;
+        if (key0 + 16 <= n0) {
+          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, 16 * warp, key0, lane);
+        } else if (key0 < keys) {
+          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, 16 * warp, key0, lane);
+        }
+        // The last warp to leave a tile fetches the stage's next one: no thread waits for a free
+        // stage.  Every warp leaves the tiles in order, so the fetches happen in order too.
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence_block();
+          if (atomicAdd(&ctl.done[stage], 1) == kWarps - 1) {
+            __threadfence_block();
+            ctl.done[stage] = 0;
+            fetch_tile<D, NT>(a, &ctl, ring, end);
+          }
+        }
+        __syncwarp();
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    const bool whole = n == u.tiles;
+    float* slot = nullptr;
+    if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(Lay::ROWS);
+    finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + STAGES * Lay::STAGE), whole, slot, warp,
+                            lane);
+    t += n;
+  }
+  if (ctl.abort && tid == 0) {  // the copies in flight land in this CTA's shared memory: wait for them
+    volatile int none = 0;
+    for (int k = max(0, ctl.fills - STAGES); k < ctl.fills; ++k)
+      tc::mbar_wait(&ctl.full[k % STAGES], (uint32_t)(k / STAGES) & 1u, &none, a.err);
+  }
+}
+
+// Units that several CTAs touched: one CTA for each query row merges their slots.
+//   M = max_c m_c,  o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int ctas) {
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  constexpr int ROWS = 8 * NT;
+  constexpr int LPR = D / 4;             // lanes of a row, four channels each
+  constexpr int LANES = 256 / LPR;       // slots read at a time
+  __shared__ int cum[kKv4AttnMaxB + 1];
+  __shared__ float4 part[LANES][LPR];
+  __shared__ float lsum[LANES];
+  __shared__ float topw[8];
+  const int tid = threadIdx.x;
+  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
+  pdl_trigger();
+  if (tid < 32) scan_tiles(a, cum, tid, false);
+  __syncthreads();
+  const int per = cum[a.B] * a.Hkv * a.row_blocks;
+  const int total = per * a.L;
+  int id = blockIdx.x;  // ((l * B + b) * Hkv + h) * rows + r
+  const int r = id % a.rows;
+  id /= a.rows;
+  const int h = id % a.Hkv, lb = id / a.Hkv, b = lb % a.B, l = lb / a.B;
+  const int tiles = cum[b + 1] - cum[b];
+  if (tiles == 0) return;
+  const int rb = r / ROWS, n = r - rb * ROWS;
+  const int u0 = l * per + cum[b] * a.Hkv * a.row_blocks + (h * a.row_blocks + rb) * tiles;
+  // the CTA that holds tile x is the last c with floor(total c / ctas) <= x
+  const int c0 = (int)((((int64_t)u0 + 1) * ctas - 1) / total);
+  const int c1 = (int)((((int64_t)u0 + tiles) * ctas - 1) / total);
+  if (c0 == c1) return;  // written whole
+  const int lane = tid % LPR, first = tid / LPR;
+  auto slot_of = [&](int c) -> const float* {
+    const int s = cta_begin(total, ctas, c);
+    if (s == cta_begin(total, ctas, c + 1)) return nullptr;
+    return a.ws + (2 * (int64_t)c + (u0 <= s ? 0 : 1)) * slot_floats<D>(ROWS);
+  };
+  float top = -INFINITY;
+  for (int c = c0 + tid; c <= c1; c += 256)
+    if (const float* p = slot_of(c)) top = fmaxf(top, p[ROWS * D + 2 * n]);
+  top = warp_max(top);
+  if ((tid & 31) == 0) topw[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, topw[w]);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lt = 0.f;
+  for (int c = c0 + first; c <= c1; c += LANES) {
+    const float* p = slot_of(c);
+    if (!p) continue;
+    const float2 ml = *reinterpret_cast<const float2*>(p + ROWS * D + 2 * n);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    const float4 v = *reinterpret_cast<const float4*>(p + n * D + 4 * lane);
+    sum.x = fmaf(f, v.x, sum.x); sum.y = fmaf(f, v.y, sum.y);
+    sum.z = fmaf(f, v.z, sum.z); sum.w = fmaf(f, v.w, sum.w);
+    lt = fmaf(f, ml.y, lt);
+  }
+  part[first][lane] = sum;
+  if (lane == 0) lsum[first] = lt;
+  __syncthreads();
+  if (tid < LPR) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < LANES; ++i) {
+      const float4 v = part[i][tid];
+      o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+      s += lsum[i];
+    }
+    const float inv = s == 0.f ? 0.f : 1.f / s;
+    const int64_t at = (((int64_t)lb * a.Hq + h * a.G) * a.nq + r) * D + 4 * tid;
+    store4(static_cast<T*>(a.o) + at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  }
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
+  using Lay = Layout<D, NT>;
+  auto* kern = kv4_attn_kernel<D, NT, F32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), Lay::BYTES, s, a);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.L * a.B * a.Hkv * a.rows;
+  return launch_pdl(kv4_merge_kernel<D, NT, F32>, dim3((unsigned)rows), dim3(256), 0, s, a, a.ctas);
+}
+
+}  // namespace
+
+// Query rows of a block, and CTAs of an SM, by the kernel the call takes.
+void plan_kv4_attn(Kv4AttnArgs* a, int sms) {
+  const int nt = a->rows <= 8 ? 1 : 2;
+  a->row_blocks = (a->rows + 8 * nt - 1) / (8 * nt);
+  const int64_t tiles = (int64_t)a->L * a->B * a->Hkv * a->row_blocks * ((a->cap + kTile - 1) / kTile);
+  const int64_t most = (int64_t)sms * (nt == 1 && a->dtype == STD_BF16 ? 2 : 1);
+  a->ctas = (int)(tiles < most ? tiles : most);
+  a->ws_floats = 2 * a->ctas * (int64_t)(8 * nt) * (a->d + 2);
+}
+
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
+  const bool one = a.rows <= 8, f32 = a.dtype == STD_F32;
+  if (a.d == 128) {
+    if (f32) return one ? launch<128, 1, true>(a, s) : launch<128, 2, true>(a, s);
+    return one ? launch<128, 1, false>(a, s) : launch<128, 2, false>(a, s);
+  }
+  if (f32) return one ? launch<64, 1, true>(a, s) : launch<64, 2, true>(a, s);
+  return one ? launch<64, 1, false>(a, s) : launch<64, 2, false>(a, s);
+}
+
+}  // namespace stdb
