@@ -2,13 +2,16 @@
 // step) up to gamma + 1 causal ones.
 //
 //   K_jc = mk_jg + sk_jg a_jc,  V_jc = mv_jg + sv_jg b_jc       codes a, b in 0..15, group g of channel c
-//   x_rj = sum_g sk_jg (q_r . (a_j - 8))_g + (mk_jg + 8 sk_jg) (sum q_r)_g          scaled by log2(e) / sqrt(d)
+//   x_rj = sum_g sk_jg (q_r . a_j)_g + mk_jg (sum q_r)_g                          scaled by log2(e) / sqrt(d)
 //   o_rc = [ sum_j (p_rj sv_jg) (b_jc - 8) + sum_j p_rj (mv_jg + 8 sv_jg) ] / sum_j p_rj,   p = 2^(x - M_r)
 //
 // so the scales never touch the codes: K's multiply the two partial dot products of a key, V's
-// multiply the weights, and what the tensor cores see of a code is the small integer c - 8,
-// exact in fp16.  (Codes are centred because sum p b would otherwise grow without bound while
-// the answer stays near the mean: at 140,000 keys the fp32 accumulator would lose it.)
+// multiply the weights.  A code enters the tensor cores as the fp16 number whose bits are the masked
+// code: a subnormal, c 2^-24 (low nibble of a byte) or c 2^-20 (high), exact in the product and in the
+// fp32 sum; powers of two in q and in the result undo it.  One mask for two codes is all that widening
+// costs.  (The sum over keys has to be centred, b - 8, because sum p b grows without bound while the
+// answer stays near the mean: at 140,000 keys the fp32 accumulator would lose it.  A product with a
+// matrix of eights, one for sixteen, gathers 8 sum p sv, and is subtracted every few tiles.)
 //
 // A byte of the cache feeds 2 G x rows multiply-adds, and a key's codes have to be widened
 // before any of them: at d = 128 a (row, head) is 144 bytes, against 512 in bf16, and its 256
@@ -38,6 +41,7 @@ constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLimit = 32768.f;        // largest weight x scale that goes to fp16
 constexpr float kSmall = 9.094947e-13f;  // 2^-40: scales below it count as this much, so that p stays below 2^55
+constexpr float kMostSum = 1.2676506e30f;  // 2^100: a sum of weights above it moves the reference too
 constexpr float kHeadroom = 8.f;         // a new reference puts the largest one at 2^8
 
 // ---------------------------------------------------------------- shared memory
@@ -57,8 +61,7 @@ struct Layout {
 
 constexpr int kMaxStages = 16;
 struct Ctl {
-  uint64_t full[kMaxStages];
-  int done[kMaxStages];  // warps that have read the stage's tile
+  uint64_t full[kMaxStages], empty[kMaxStages];
   // the next tile to fetch (touched only by the thread that fetches it)
   int fills, next, left, first, keys;
   int64_t row0;  // cache row of the unit's row 0
@@ -140,6 +143,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {  // d = a b
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // 16-bit elements, rows over lane / 4
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -148,14 +157,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // 16-bit elemen
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-// Codes to fp16: 0x6400 is 1024, whose last ten bits hold a code at bit 0 (1024 + c) or at
-// bit 4 (1024 + 16 c); one exact subtraction or fused multiply-add leaves c - 8.
-__device__ __forceinline__ uint32_t widen0(uint32_t w) {  // bits 0-3 and 16-19
-  return as_u32(__hsub2(as_h2((w & 0x000f000fu) | 0x64006400u), __float2half2_rn(1032.f)));
-}
-__device__ __forceinline__ uint32_t widen4(uint32_t w) {  // bits 4-7 and 20-23
-  return as_u32(__hfma2(as_h2((w & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
-}
+// Two codes as fp16 subnormals: c 2^-24 from bits 0-3 and 16-19, c 2^-20 from bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
+constexpr uint32_t kEight0 = 0x00080008u, kEight4 = 0x00800080u;  // the code 8 in either place
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -173,7 +178,22 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ float max_of(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts_f2(uint32_t a, float2 v) {
+  asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
 __device__ __forceinline__ float column_sum(float v) {  // over the eight lanes of one accumulator column
   v += __shfl_xor_sync(0xffffffffu, v, 4);
   v += __shfl_xor_sync(0xffffffffu, v, 8);
@@ -203,7 +223,8 @@ struct State {
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
   int lim[NT][2];                            // keys the row attends
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
-  float o[NT][MT][4];                        // sum (p sv) (b - 8)
+  float o[NT][MT][4];                        // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8)
+  float eight[NT][GR][4];                    // sum (p sv) 8 of the same keys since the last settle(), same units
 };
 
 template <int D, int NT, bool F32>
@@ -241,8 +262,8 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[w][i]));
     }
     top = quad_max(top);
-    // scale the row by a power of two that puts its largest entry in [2^14, 2^15): exact, and
-    // entries down to 2^-28 of it keep all their bits in fp16
+    // scale the row by a power of two that puts its largest entry in [2^14, 2^15), a sixteenth of that
+    // where it meets codes at 2^-20: exact, and entries down to 2^-24 of it keep all their bits
     int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
     ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;
     const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
@@ -260,18 +281,20 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // channels 2 k + e and 2 k + e + 4 of the word: one register pair
-          const __half2 hv = __floats2half2_rn(x[w][2 * k + e], x[w][2 * k + e + 4]);
+          const float x0 = x[w][2 * k + e] * (e ? 0.0625f : 1.f), x1 = x[w][2 * k + e + 4] * (e ? 0.0625f : 1.f);
+          const __half2 hv = __floats2half2_rn(x0, x1);
           st.qh[nt][2 * w + k][e] = as_u32(hv);
           if constexpr (F32) {
             const float2 f = __half22float2(hv);
-            st.ql[nt][2 * w + k][e] =
-                as_u32(__floats2half2_rn(x[w][2 * k + e] - f.x, x[w][2 * k + e + 4] - f.y));
+            st.ql[nt][2 * w + k][e] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
           }
         }
     }
-    const float back = scale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+    // the products come out in units of 2^(ex - 14) 2^24
+    const float back = scale * __uint_as_float((uint32_t)(ex + 10 - (ex > 100 ? 20 : 0) + 127) << 23) *
+                       (ex > 100 ? 1048576.f : 1.f);
 #pragma unroll
-    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]);
+    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]) * 5.9604645e-8f;  // 2^-24
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int from = 4 * (2 * t + e);  // a lane that holds row 2 t + e
@@ -286,32 +309,61 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       for (int gr = 0; gr < S::GR; ++gr) st.pm[nt][gr][e] = 0.f;
     }
 #pragma unroll
-    for (int mt = 0; mt < S::MT; ++mt)
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.o[nt][mt][i] = 0.f;
+      for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr) st.eight[nt][gr][i] = 0.f;
+    }
   }
 }
 
+// Centre the sums gathered since the last call.
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void settle(State<D, NT, F32>& st) {
+  using S = State<D, NT, F32>;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] -= st.eight[nt][mt / 4][i];
+#pragma unroll
+      for (int gr = 0; gr < S::GR; ++gr) st.eight[nt][gr][i] = 0.f;
+    }
+}
+
 // 16 keys: rows [row0, row0 + 16) of the tile at shared addresses kc / vc / ks / vs, key0 = the
-// first one's position.  MASK: some of them may lie past a row's limit (or past the cache,
-// where the shared memory holds stale bytes: codes are finite whatever they are, scales are not).
+// first one's position.  scratch: 512 bytes of this warp's.  MASK: some of the keys may lie past a
+// row's limit (or past the cache, where the shared memory holds stale bytes: codes are finite
+// whatever they are, scales are not).
 template <int D, int NT, bool F32, bool MASK>
 __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uint32_t vc, uint32_t ks, uint32_t vs,
-                                         int row0, int key0, int lane) {
+                                         uint32_t scratch, int row0, int key0, int lane) {
   using S = State<D, NT, F32>;
   using Lay = Layout<D, NT>;
   constexpr int GR = S::GR, WPL = D / 32;
   const int g = lane >> 2, t = lane & 3;
   const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);  // key of accumulator row g; row g + 8 is 8 higher
 
-  // S^T: two partial products, one for each group
+  // The 16 keys' scales to fp32, one half-warp for K and one for V, (s, m) of both groups: each lane
+  // needs two keys' of each, and four lanes the same ones.
+  {
+    const uint32_t at = (lane < 16 ? ks : vs) + (row0 + (lane & 15)) * Lay::SW;
+    const float c = lane < 16 ? 0.f : 8.f;
+    if constexpr (GR == 2) {
+      const uint2 u = lds64(at);
+      const float s0 = lo_bf16(u.x), s1 = lo_bf16(u.y);
+      sts_f4(scratch + lane * 16, make_float4(s0, s1, fmaf(c, s0, hi_bf16(u.x)), fmaf(c, s1, hi_bf16(u.y))));
+    } else {
+      const uint32_t u = lds32(at);
+      const float s0 = lo_bf16(u);
+      sts_f2(scratch + lane * 8, make_float2(s0, fmaf(c, s0, hi_bf16(u))));
+    }
+  }
+
+  // S^T: a partial product for each group
   float acc[NT][GR][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][gr][i] = 0.f;
   uint32_t wa[WPL], wb[WPL];
   {
     const uint32_t ra = kc + (row0 + kap) * Lay::CW + t * (WPL * 4), rb = ra + 8 * Lay::CW;
@@ -334,74 +386,85 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
       const uint32_t a0 = widen0(x), a1 = widen0(y), a2 = widen4(x), a3 = widen4(y);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_f16(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
+        if (w < GR && k == 0)
+          mma_f16_zero(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
+        else
+          mma_f16(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
         if constexpr (F32) mma_f16(acc[nt][gr], a0, a1, a2, a3, st.ql[nt][2 * w + k][0], st.ql[nt][2 * w + k][1]);
       }
     }
   }
 
-  // scales of keys kap and kap + 8
-  float sk[2][GR], mk[2][GR], sv[2][GR], mv[2][GR], smax[2];
+  __syncwarp();
+  float sk[2][GR], mk[2][GR], sv[2][GR], mv[2][GR];  // of keys kap and kap + 8
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    const uint32_t at = (row0 + kap + 8 * hf) * Lay::SW;
-    uint32_t uk[GR], uv[GR];
     if constexpr (GR == 2) {
-      const uint2 x = lds64(ks + at), y = lds64(vs + at);
-      uk[0] = x.x; uk[1] = x.y; uv[0] = y.x; uv[1] = y.y;
+      const float4 x = lds_f4(scratch + (kap + 8 * hf) * 16), y = lds_f4(scratch + (16 + kap + 8 * hf) * 16);
+      sk[hf][0] = x.x; sk[hf][1] = x.y; mk[hf][0] = x.z; mk[hf][1] = x.w;
+      sv[hf][0] = y.x; sv[hf][1] = y.y; mv[hf][0] = y.z; mv[hf][1] = y.w;
     } else {
-      uk[0] = lds32(ks + at);
-      uv[0] = lds32(vs + at);
+      const float2 x = lds_f2(scratch + (kap + 8 * hf) * 8), y = lds_f2(scratch + (16 + kap + 8 * hf) * 8);
+      sk[hf][0] = x.x; mk[hf][0] = x.y; sv[hf][0] = y.x; mv[hf][0] = y.y;
     }
-#pragma unroll
-    for (int gr = 0; gr < GR; ++gr) {
-      sk[hf][gr] = lo_bf16(uk[gr]);
-      mk[hf][gr] = fmaf(8.f, sk[hf][gr], hi_bf16(uk[gr]));
-      sv[hf][gr] = lo_bf16(uv[gr]);
-      mv[hf][gr] = fmaf(8.f, sv[hf][gr], hi_bf16(uv[gr]));
-    }
-    smax[hf] = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
   }
 
-  // logits (log2 domain); element i of an accumulator: key half i / 2, row 2 t + i % 2
-  float x[NT][4];
+  // Logits and weights against the running reference M.  Element i of an accumulator: key half
+  // i / 2, row 2 t + i % 2.  w = p sv has to fit fp16 and the sum of p fp32; where they do not (or no
+  // reference is set yet) the references of this warp's rows move up and the weights are taken again.
+  float p[NT][4], wt[NT][GR][4], l[NT][2];
   bool seen[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  auto weigh = [&](int nt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int hf = i >> 1, e = i & 1;
       float y = 0.f;
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
-        y = fmaf(sk[hf][gr], acc[nt][gr][i], y);
+        y = gr == 0 ? sk[hf][0] * acc[nt][0][i] : fmaf(sk[hf][gr], acc[nt][gr][i], y);
         y = fmaf(mk[hf][gr], st.qsum[nt][gr][e], y);
       }
-      x[nt][i] = y * st.rs[nt][e];
-      seen[nt][i] = !MASK || key0 + kap + 8 * hf < st.lim[nt][e];
+      p[nt][i] = ex2(fmaf(y, st.rs[nt][e], -st.M[nt][e]));
+      if constexpr (MASK) {
+        seen[nt][i] = key0 + kap + 8 * hf < st.lim[nt][e];
+        if (!seen[nt][i]) p[nt][i] = 0.f;
+      }
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) {
+        wt[nt][gr][i] = p[nt][i] * sv[hf][gr];
+        if (MASK && !seen[nt][i]) wt[nt][gr][i] = 0.f;  // (a scale past the limit may be anything)
+      }
     }
-
-  // weights against the running reference M; p sv has to fit fp16, and where it does not (or
-  // no reference is set yet) the references of this warp's rows move up first
-  float p[NT][4];
-  float big = 0.f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) l[nt][e] = st.l[nt][e] + (p[nt][e] + p[nt][2 + e]);
+  };
+  float big = 0.f, lbig = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[nt][i] = ex2(x[nt][i] - st.M[nt][i & 1]);
-      if (seen[nt][i] && !(p[nt][i] * smax[i >> 1] <= kLimit)) big = 1.f;  // (a NaN counts)
+  for (int nt = 0; nt < NT; ++nt) {
+    weigh(nt);
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr) {
+      const float m0 = nt + gr == 0 ? wt[nt][gr][0] : fmaxf(big, wt[nt][gr][0]);
+      big = max3f(max3f(m0, wt[nt][gr][1], wt[nt][gr][2]), wt[nt][gr][3], m0);
     }
-  if (__any_sync(0xffffffffu, big != 0.f)) {
+    lbig = max3f(lbig, l[nt][0], l[nt][1]);
+  }
+  // (a NaN among others is the data's; where all weights are NaN, 0 x infinity, no reference is set)
+  if (__any_sync(0xffffffffu, !(big <= kLimit) || !(lbig <= kMostSum))) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float z = -INFINITY;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          if (seen[nt][2 * hf + e])
-            z = fmaxf(z, x[nt][2 * hf + e] + __log2f(smax[hf]));
+        for (int hf = 0; hf < 2; ++hf) {
+          float y = 0.f;
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+            y = fmaf(sk[hf][gr], acc[nt][gr][2 * hf + e], fmaf(mk[hf][gr], st.qsum[nt][gr][e], y));
+          const float big_s = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
+          if (!MASK || seen[nt][2 * hf + e]) z = fmaxf(z, y * st.rs[nt][e] + __log2f(big_s));
+        }
         z = column_max(z);
         if (z - st.M[nt][e] > 14.9f) {
           const float m1 = z - kHeadroom;
@@ -409,39 +472,35 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
           st.M[nt][e] = m1;
           st.l[nt][e] *= f;
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) st.pm[nt][gr][e] *= f;
+          for (int gr = 0; gr < GR; ++gr) {
+            st.pm[nt][gr][e] *= f;
+            st.eight[nt][gr][e] *= f;
+            st.eight[nt][gr][2 + e] *= f;
+          }
 #pragma unroll
           for (int mt = 0; mt < S::MT; ++mt) {
             st.o[nt][mt][e] *= f;
             st.o[nt][mt][2 + e] *= f;
           }
         }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) p[nt][2 * hf + e] = ex2(x[nt][2 * hf + e] - st.M[nt][e]);
       }
+      weigh(nt);
+    }
   }
 
   // P^T operands: rows of a key pack side by side, and an 8 x 8 transposition puts keys there
   uint32_t ph[NT][GR][2], pl[F32 ? NT : 1][F32 ? GR : 1][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (MASK && !seen[nt][i]) p[nt][i] = 0.f;
-      st.l[nt][i & 1] += p[nt][i];
-    }
+    st.l[nt][0] = l[nt][0];
+    st.l[nt][1] = l[nt][1];
 #pragma unroll
     for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float w0 = p[nt][2 * hf] * sv[hf][gr], w1 = p[nt][2 * hf + 1] * sv[hf][gr];
-        float c0 = p[nt][2 * hf] * mv[hf][gr], c1 = p[nt][2 * hf + 1] * mv[hf][gr];
-        if constexpr (MASK) {  // a scale past the limit may be anything
-          if (!seen[nt][2 * hf]) w0 = c0 = 0.f;
-          if (!seen[nt][2 * hf + 1]) w1 = c1 = 0.f;
-        }
-        st.pm[nt][gr][0] += c0;
-        st.pm[nt][gr][1] += c1;
+        const float w0 = wt[nt][gr][2 * hf], w1 = wt[nt][gr][2 * hf + 1];
+        if (!MASK || seen[nt][2 * hf]) st.pm[nt][gr][0] = fmaf(p[nt][2 * hf], mv[hf][gr], st.pm[nt][gr][0]);
+        if (!MASK || seen[nt][2 * hf + 1]) st.pm[nt][gr][1] = fmaf(p[nt][2 * hf + 1], mv[hf][gr], st.pm[nt][gr][1]);
         const __half2 hv = __floats2half2_rn(w0, w1);
         ph[nt][gr][hf] = transpose8x8(as_u32(hv));
         if constexpr (F32) {
@@ -449,6 +508,11 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
           pl[nt][gr][hf] = transpose8x8(as_u32(__floats2half2_rn(w0 - f.x, w1 - f.y)));
         }
       }
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr) {
+      mma_f16(st.eight[nt][gr], kEight0, kEight4, kEight0, kEight4, ph[nt][gr][0], ph[nt][gr][1]);
+      if constexpr (F32) mma_f16(st.eight[nt][gr], kEight0, kEight4, kEight0, kEight4, pl[nt][gr][0], pl[nt][gr][1]);
+    }
   }
 
   // O^T += V^T P^T: lane t's keys, two words (d = 128: one of each group) of 8 channels at 8 g
@@ -507,6 +571,8 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
   using Lay = Layout<D, NT>;
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   const int g = lane >> 2, t = lane & 3;
+  settle(st);
+  compute_sync();  // (the merge buffer's first bytes were the loop's scratch)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -517,8 +583,8 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
         const float c = column_sum(st.pm[nt][gr][e]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          st.o[nt][gr * 4 + i][e] += c;
-          st.o[nt][gr * 4 + i][2 + e] += c;
+          st.o[nt][gr * 4 + i][e] = fmaf(st.o[nt][gr * 4 + i][e], 16777216.f, c);         // 2^24
+          st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], 1048576.f, c);  // 2^20
         }
       }
       if (g == 0) {
@@ -616,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&ctl.full[s], 1);
-      ctl.done[s] = 0;
+      tc::mbar_init(&ctl.empty[s], kWarps);
     }
     ctl.abort = 0;
     ctl.fills = ctl.left = 0;
@@ -634,8 +700,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     ctl.next = begin;
     for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT>(a, &ctl, ring, end);
   }
-  int stage = 0;
+  const uint32_t scratch = ring + STAGES * Lay::STAGE + warp * 512;
+  int stage = 0, turn = 0;  // turn: the warp that fetches after this tile
   uint32_t phase = 0;
+  bool more = false;  // there is a tile before this one
   State<D, NT, F32> st;
   bool ok = true;
   for (int t = begin; t < end;) {
@@ -654,26 +722,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
                        vs = ks + kTile * Lay::SW;
         const int key0 = first + 16 * warp;
         if (key0 + 16 <= n0) {
-          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, 16 * warp, key0, lane);
+          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, lane);
         } else if (key0 < keys) {
-          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, 16 * warp, key0, lane);
+          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, lane);
         }
-        // The last warp to leave a tile fetches the stage's next one: no thread waits for a free
-        // stage.  Every warp leaves the tiles in order, so the fetches happen in order too.
+        // The warps take turns to fetch: into the stage of the tile before this one, which the others
+        // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
+        // happen one at a time and in order.
         __syncwarp();
         if (lane == 0) {
-          __threadfence_block();
-          if (atomicAdd(&ctl.done[stage], 1) == kWarps - 1) {
-            __threadfence_block();
-            ctl.done[stage] = 0;
-            fetch_tile<D, NT>(a, &ctl, ring, end);
+          if (turn == warp && more) {
+            const int before = stage == 0 ? STAGES - 1 : stage - 1;
+            if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
+              fetch_tile<D, NT>(a, &ctl, ring, end);
           }
+          tc::mbar_arrive(&ctl.empty[stage]);
         }
         __syncwarp();
+        more = true;
+        turn = (turn + 1) & (kWarps - 1);
       }
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1;
+        settle(st);
       }
     }
     const bool whole = n == u.tiles;
