@@ -219,69 +219,75 @@ struct State {
   static constexpr int MT = D / 16;          // 16-channel tiles of O^T
   uint32_t qh[NT][KS][2];                    // q, scaled by a power of two, as the B operand
   uint32_t ql[F32 ? NT : 1][F32 ? KS : 1][2];  // its remainder below fp16 (fp32 queries)
-  float rs[NT][2];                           // x = rs * (K . scaled q)
+  float back;                                // K's scales times this: undoes q's scaling, log2(e) / sqrt(d)
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
-  int lim[NT][2];                            // keys the row attends
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
   float o[NT][MT][4];                        // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8)
   float eight[NT][GR][4];                    // sum (p sv) 8 of the same keys since the last settle(), same units
 };
 
 template <int D, int NT, bool F32>
-__device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, int n0,
-                                             int lane) {
+__device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, int lane) {
   using S = State<D, NT, F32>;
   const int g = lane >> 2, t = lane & 3;
   constexpr int WPL = D / 32;  // words of a row that lane t multiplies
-  const float scale = kLog2e * rsqrtf((float)D);
+  float x[NT][WPL][8];
+  float top = 0.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = u.rb * 8 * NT + nt * 8 + g;
-    float x[WPL][8];
-    float top = 0.f;
 #pragma unroll
     for (int w = 0; w < WPL; ++w) {
       const int ch = kv4_word_channel<D>(WPL * t + w);
+      float(&y)[8] = x[nt][w];
       if (r < a.rows) {
         const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + ch;
         if constexpr (F32) {
           const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
           const float4 v0 = p[0], v1 = p[1];
-          x[w][0] = v0.x; x[w][1] = v0.y; x[w][2] = v0.z; x[w][3] = v0.w;
-          x[w][4] = v1.x; x[w][5] = v1.y; x[w][6] = v1.z; x[w][7] = v1.w;
+          y[0] = v0.x; y[1] = v0.y; y[2] = v0.z; y[3] = v0.w;
+          y[4] = v1.x; y[5] = v1.y; y[6] = v1.z; y[7] = v1.w;
         } else {
           const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-          x[w][0] = lo_bf16(v.x); x[w][1] = hi_bf16(v.x); x[w][2] = lo_bf16(v.y); x[w][3] = hi_bf16(v.y);
-          x[w][4] = lo_bf16(v.z); x[w][5] = hi_bf16(v.z); x[w][6] = lo_bf16(v.w); x[w][7] = hi_bf16(v.w);
+          y[0] = lo_bf16(v.x); y[1] = hi_bf16(v.x); y[2] = lo_bf16(v.y); y[3] = hi_bf16(v.y);
+          y[4] = lo_bf16(v.z); y[5] = hi_bf16(v.z); y[6] = lo_bf16(v.w); y[7] = hi_bf16(v.w);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[w][i] = 0.f;
+        for (int i = 0; i < 8; ++i) y[i] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[w][i]));
+      for (int i = 0; i < 8; ++i)
+        if (fabsf(y[i]) < INFINITY) top = fmaxf(top, fabsf(y[i]));  // (a row with an infinity gives NaN by itself)
     }
-    top = quad_max(top);
-    // scale the row by a power of two that puts its largest entry in [2^14, 2^15), a sixteenth of that
-    // where it meets codes at 2^-20: exact, and entries down to 2^-24 of it keep all their bits
-    int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-    ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;
-    const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+  }
+  top = warp_max(top);
+  // Scale the block by a power of two that puts its largest entry in [2^14, 2^15), a sixteenth of that
+  // where it meets codes at 2^-20: exact, and entries down to 2^-24 of it keep all their bits.
+  int ex = (int)(__float_as_uint(top) >> 23) - 127;
+  ex = ex < -100 ? -100 : ex;
+  const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+  // the products come out in units of 2^(ex - 14) 2^24
+  st.back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)((ex > 100 ? ex - 10 : ex + 10) + 127) << 23);
+  if (ex > 100) st.back *= 1048576.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     float sum[S::GR];
 #pragma unroll
     for (int gr = 0; gr < S::GR; ++gr) sum[gr] = 0.f;
 #pragma unroll
     for (int w = 0; w < WPL; ++w) {
+      float(&y)[8] = x[nt][w];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[w][i] *= mul;
-        sum[S::GR == 2 ? (w & 1) : 0] += x[w][i];
+        y[i] *= mul;
+        sum[S::GR == 2 ? (w & 1) : 0] += y[i];
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // channels 2 k + e and 2 k + e + 4 of the word: one register pair
-          const float x0 = x[w][2 * k + e] * (e ? 0.0625f : 1.f), x1 = x[w][2 * k + e + 4] * (e ? 0.0625f : 1.f);
+          const float x0 = y[2 * k + e] * (e ? 0.0625f : 1.f), x1 = y[2 * k + e + 4] * (e ? 0.0625f : 1.f);
           const __half2 hv = __floats2half2_rn(x0, x1);
           st.qh[nt][2 * w + k][e] = as_u32(hv);
           if constexpr (F32) {
@@ -290,19 +296,13 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
           }
         }
     }
-    // the products come out in units of 2^(ex - 14) 2^24
-    const float back = scale * __uint_as_float((uint32_t)(ex + 10 - (ex > 100 ? 20 : 0) + 127) << 23) *
-                       (ex > 100 ? 1048576.f : 1.f);
 #pragma unroll
     for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]) * 5.9604645e-8f;  // 2^-24
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int from = 4 * (2 * t + e);  // a lane that holds row 2 t + e
-      st.rs[nt][e] = __shfl_sync(0xffffffffu, back, from);
 #pragma unroll
       for (int gr = 0; gr < S::GR; ++gr) st.qsum[nt][gr][e] = __shfl_sync(0xffffffffu, sum[gr], from);
-      const int row = u.rb * 8 * NT + nt * 8 + 2 * t + e;
-      st.lim[nt][e] = n0 + (row < a.rows ? row % a.nq : 0);
       st.M[nt][e] = -INFINITY;
       st.l[nt][e] = 0.f;
 #pragma unroll
@@ -335,30 +335,42 @@ __device__ __forceinline__ void settle(State<D, NT, F32>& st) {
 
 // 16 keys: rows [row0, row0 + 16) of the tile at shared addresses kc / vc / ks / vs, key0 = the
 // first one's position.  scratch: 512 bytes of this warp's.  MASK: some of the keys may lie past a
-// row's limit (or past the cache, where the shared memory holds stale bytes: codes are finite
-// whatever they are, scales are not).
+// row's limit, n0 for query position 0 (or past the cache, where the shared memory holds stale bytes:
+// codes are finite whatever they are, scales are not).
 template <int D, int NT, bool F32, bool MASK>
 __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uint32_t vc, uint32_t ks, uint32_t vs,
-                                         uint32_t scratch, int row0, int key0, int lane) {
+                                         uint32_t scratch, int row0, int key0, int n0, int rb, int nq, int rows,
+                                         int lane) {
   using S = State<D, NT, F32>;
   using Lay = Layout<D, NT>;
   constexpr int GR = S::GR, WPL = D / 32;
   const int g = lane >> 2, t = lane & 3;
   const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);  // key of accumulator row g; row g + 8 is 8 higher
 
+  int lim[NT][2];  // keys the row attends
+  if constexpr (MASK) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = (rb * NT + nt) * 8 + 2 * t + e;
+        lim[nt][e] = n0 + (row < rows ? row % nq : 0);
+      }
+  }
   // The 16 keys' scales to fp32, one half-warp for K and one for V, (s, m) of both groups: each lane
   // needs two keys' of each, and four lanes the same ones.
   {
     const uint32_t at = (lane < 16 ? ks : vs) + (row0 + (lane & 15)) * Lay::SW;
-    const float c = lane < 16 ? 0.f : 8.f;
+    const float c = lane < 16 ? 0.f : 8.f, f = lane < 16 ? st.back : 1.f;
     if constexpr (GR == 2) {
       const uint2 u = lds64(at);
       const float s0 = lo_bf16(u.x), s1 = lo_bf16(u.y);
-      sts_f4(scratch + lane * 16, make_float4(s0, s1, fmaf(c, s0, hi_bf16(u.x)), fmaf(c, s1, hi_bf16(u.y))));
+      sts_f4(scratch + lane * 16,
+             make_float4(f * s0, f * s1, f * fmaf(c, s0, hi_bf16(u.x)), f * fmaf(c, s1, hi_bf16(u.y))));
     } else {
       const uint32_t u = lds32(at);
       const float s0 = lo_bf16(u);
-      sts_f2(scratch + lane * 8, make_float2(s0, fmaf(c, s0, hi_bf16(u))));
+      sts_f2(scratch + lane * 8, make_float2(f * s0, f * fmaf(c, s0, hi_bf16(u))));
     }
   }
 
@@ -418,15 +430,15 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int hf = i >> 1, e = i & 1;
-      float y = 0.f;
+      float x = -st.M[nt][e];
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
-        y = gr == 0 ? sk[hf][0] * acc[nt][0][i] : fmaf(sk[hf][gr], acc[nt][gr][i], y);
-        y = fmaf(mk[hf][gr], st.qsum[nt][gr][e], y);
+        x = fmaf(mk[hf][gr], st.qsum[nt][gr][e], x);
+        x = fmaf(sk[hf][gr], acc[nt][gr][i], x);
       }
-      p[nt][i] = ex2(fmaf(y, st.rs[nt][e], -st.M[nt][e]));
+      p[nt][i] = ex2(x);
       if constexpr (MASK) {
-        seen[nt][i] = key0 + kap + 8 * hf < st.lim[nt][e];
+        seen[nt][i] = key0 + kap + 8 * hf < lim[nt][e];
         if (!seen[nt][i]) p[nt][i] = 0.f;
       }
 #pragma unroll
@@ -458,12 +470,12 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
         float z = -INFINITY;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float y = 0.f;
+          float x = 0.f;
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr)
-            y = fmaf(sk[hf][gr], acc[nt][gr][2 * hf + e], fmaf(mk[hf][gr], st.qsum[nt][gr][e], y));
+            x = fmaf(sk[hf][gr], acc[nt][gr][2 * hf + e], fmaf(mk[hf][gr], st.qsum[nt][gr][e], x));
           const float big_s = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
-          if (!MASK || seen[nt][2 * hf + e]) z = fmaxf(z, y * st.rs[nt][e] + __log2f(big_s));
+          if (!MASK || seen[nt][2 * hf + e]) z = fmaxf(z, x + __log2f(big_s));
         }
         z = column_max(z);
         if (z - st.M[nt][e] > 14.9f) {
@@ -701,37 +713,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT>(a, &ctl, ring, end);
   }
   const uint32_t scratch = ring + STAGES * Lay::STAGE + warp * 512;
-  int stage = 0, turn = 0;  // turn: the warp that fetches after this tile
+  int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
   uint32_t phase = 0;
-  bool more = false;  // there is a tile before this one
-  State<D, NT, F32> st;
   bool ok = true;
   for (int t = begin; t < end;) {
-    const Unit u = locate(a, ctl.cum, t);
-    const int n = min(u.tiles - u.tile0, end - t);
-    int keys = 0;
-    seq_tiles(a, u.b, &keys);
-    const int n0 = keys - a.nq + 1;  // keys that query position 0 attends
-    load_queries<D, NT, F32>(st, a, u, n0, lane);
-    for (int i = 0; i < n; ++i) {
-      const int first = (u.tile0 + i) * kTile;
-      if (first >= keys) break;
+    State<D, NT, F32> st;
+    int key0, n0, left, rb;
+    {
+      const Unit u = locate(a, ctl.cum, t);
+      int keys = 0;
+      seq_tiles(a, u.b, &keys);
+      key0 = u.tile0 * kTile;
+      left = min(min(u.tiles - u.tile0, end - t), (keys - key0 + kTile - 1) / kTile);  // (no keys: no tile to read)
+      n0 = keys - a.nq + 1;  // keys that query position 0 attends
+      rb = u.rb;
+      load_queries<D, NT, F32>(st, a, u, lane);
+    }
+    key0 += 16 * warp;
+    for (; left > 0; --left, key0 += kTile) {
       ok = ok && tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err);
       if (ok) {
         const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
                        vs = ks + kTile * Lay::SW;
-        const int key0 = first + 16 * warp;
         if (key0 + 16 <= n0) {
-          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, lane);
-        } else if (key0 < keys) {
-          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, lane);
+          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
+        } else if (key0 < n0 + a.nq - 1) {
+          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows, lane);
         }
         // The warps take turns to fetch: into the stage of the tile before this one, which the others
         // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
         // happen one at a time and in order.
         __syncwarp();
         if (lane == 0) {
-          if (turn == warp && more) {
+          if (turn == warp) {
             const int before = stage == 0 ? STAGES - 1 : stage - 1;
             if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
               fetch_tile<D, NT>(a, &ctl, ring, end);
@@ -739,7 +753,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
           tc::mbar_arrive(&ctl.empty[stage]);
         }
         __syncwarp();
-        more = true;
         turn = (turn + 1) & (kWarps - 1);
       }
       if (++stage == STAGES) {
@@ -748,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
         settle(st);
       }
     }
+    const Unit u = locate(a, ctl.cum, t);
+    const int n = min(u.tiles - u.tile0, end - t);
     const bool whole = n == u.tiles;
     float* slot = nullptr;
     if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(Lay::ROWS);
