@@ -45,7 +45,7 @@ constexpr float kMostSum = 1.2676506e30f;  // 2^100: a sum of weights above it m
 constexpr float kHeadroom = 8.f;         // a new reference puts the largest one at 2^8
 
 // ---------------------------------------------------------------- shared memory
-template <int D, int NT>
+template <int D, int NT, bool F32>
 struct Layout {
   static constexpr int CW = D / 2;                      // code bytes of a row
   static constexpr int SW = D / kKv4Group * 4;          // scale bytes of a row
@@ -53,10 +53,13 @@ struct Layout {
   static constexpr int ROWS = 8 * NT;
   static constexpr int OSTR = D + 4;                    // row stride of the merge buffer, floats
   static constexpr int MERGE = kWarps * ROWS * OSTR * 4;
-  static constexpr int BUDGET = NT == 1 ? 108 * 1024 : 216 * 1024;
-  static constexpr int FIT = (BUDGET - MERGE) / STAGE;
+  static constexpr int QREGS = NT * (D / 16) * 2;       // a lane's query operands
+  static constexpr int Q = QREGS * 128 * (F32 ? 2 : 1);
+  static constexpr int BUDGET = NT == 1 && !F32 ? 110 * 1024 : 221 * 1024;
+  static constexpr int FIT = (BUDGET - MERGE - Q) / STAGE;
   static constexpr int STAGES = FIT < 16 ? FIT : 16;
-  static constexpr int BYTES = STAGES * STAGE + MERGE;
+  static constexpr int AT_Q = STAGES * STAGE, AT_MERGE = AT_Q + Q;
+  static constexpr int BYTES = AT_MERGE + MERGE;
 };
 
 constexpr int kMaxStages = 16;
@@ -191,6 +194,9 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
 __device__ __forceinline__ void sts_f4(uint32_t a, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 __device__ __forceinline__ void sts_f2(uint32_t a, float2 v) {
   asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
@@ -217,8 +223,8 @@ struct State {
   static constexpr int KS = D / 16;          // k-steps of S^T
   static constexpr int GR = D / kKv4Group;   // groups
   static constexpr int MT = D / 16;          // 16-channel tiles of O^T
-  uint32_t qh[NT][KS][2];                    // q, scaled by a power of two, as the B operand
-  uint32_t ql[F32 ? NT : 1][F32 ? KS : 1][2];  // its remainder below fp16 (fp32 queries)
+  // The queries, scaled by a power of two, are B operands in shared memory, four registers of a lane
+  // together: [NT][KS / 2][32 lanes][4], and for fp32 queries what is below fp16 behind them.
   float back;                                // K's scales times this: undoes q's scaling, log2(e) / sqrt(d)
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
@@ -227,7 +233,8 @@ struct State {
 };
 
 template <int D, int NT, bool F32>
-__device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, int lane) {
+__device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, uint32_t qs,
+                                             bool store, int lane) {
   using S = State<D, NT, F32>;
   const int g = lane >> 2, t = lane & 3;
   constexpr int WPL = D / 32;  // words of a row that lane t multiplies
@@ -283,18 +290,20 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
         y[i] *= mul;
         sum[S::GR == 2 ? (w & 1) : 0] += y[i];
       }
+      if (store) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // channels 2 k + e and 2 k + e + 4 of the word: one register pair
-          const float x0 = y[2 * k + e] * (e ? 0.0625f : 1.f), x1 = y[2 * k + e + 4] * (e ? 0.0625f : 1.f);
+        for (int i = 0; i < 4; ++i) {  // channels i and i + 4 of the word: one register; odd i meet codes at 2^-20
+          const float x0 = y[i] * (i & 1 ? 0.0625f : 1.f), x1 = y[i + 4] * (i & 1 ? 0.0625f : 1.f);
           const __half2 hv = __floats2half2_rn(x0, x1);
-          st.qh[nt][2 * w + k][e] = as_u32(hv);
-          if constexpr (F32) {
-            const float2 f = __half22float2(hv);
-            st.ql[nt][2 * w + k][e] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
-          }
+          const float2 f = __half22float2(hv);
+          hi[i] = as_u32(hv);
+          lo[i] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
         }
+        const uint32_t at = qs + ((nt * WPL + w) * 32 + lane) * 16;
+        sts128(at, hi);
+        if constexpr (F32) sts128(at + NT * WPL * 512, lo);
+      }
     }
 #pragma unroll
     for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]) * 5.9604645e-8f;  // 2^-24
@@ -339,10 +348,10 @@ __device__ __forceinline__ void settle(State<D, NT, F32>& st) {
 // codes are finite whatever they are, scales are not).
 template <int D, int NT, bool F32, bool MASK>
 __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uint32_t vc, uint32_t ks, uint32_t vs,
-                                         uint32_t scratch, int row0, int key0, int n0, int rb, int nq, int rows,
+                                         uint32_t qs, uint32_t scratch, int row0, int key0, int n0, int rb, int nq, int rows,
                                          int lane) {
   using S = State<D, NT, F32>;
-  using Lay = Layout<D, NT>;
+  using Lay = Layout<D, NT, F32>;
   constexpr int GR = S::GR, WPL = D / 32;
   const int g = lane >> 2, t = lane & 3;
   const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);  // key of accumulator row g; row g + 8 is 8 higher
@@ -389,23 +398,38 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
       wb[0] = y.x; wb[1] = y.y;
     }
   }
+  // (two chains of products for each partial sum: half the latency)
+  float acc2[NT][GR][4];
 #pragma unroll
   for (int w = 0; w < WPL; ++w) {
     const int gr = GR == 2 ? (w & 1) : 0;
+    uint4 qh[NT], ql[F32 ? NT : 1];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      qh[nt] = lds128(qs + ((nt * WPL + w) * 32 + lane) * 16);
+      if constexpr (F32) ql[nt] = lds128(qs + (((NT + nt) * WPL + w) * 32 + lane) * 16);
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t x = k ? wa[w] >> 8 : wa[w], y = k ? wb[w] >> 8 : wb[w];
       const uint32_t a0 = widen0(x), a1 = widen0(y), a2 = widen4(x), a3 = widen4(y);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (w < GR && k == 0)
-          mma_f16_zero(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
+        float(&c)[4] = k ? acc2[nt][gr] : acc[nt][gr];
+        if (w < GR)
+          mma_f16_zero(c, a0, a1, a2, a3, k ? qh[nt].z : qh[nt].x, k ? qh[nt].w : qh[nt].y);
         else
-          mma_f16(acc[nt][gr], a0, a1, a2, a3, st.qh[nt][2 * w + k][0], st.qh[nt][2 * w + k][1]);
-        if constexpr (F32) mma_f16(acc[nt][gr], a0, a1, a2, a3, st.ql[nt][2 * w + k][0], st.ql[nt][2 * w + k][1]);
+          mma_f16(c, a0, a1, a2, a3, k ? qh[nt].z : qh[nt].x, k ? qh[nt].w : qh[nt].y);
+        if constexpr (F32) mma_f16(c, a0, a1, a2, a3, k ? ql[nt].z : ql[nt].x, k ? ql[nt].w : ql[nt].y);
       }
     }
   }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][gr][i] += acc2[nt][gr][i];
 
   __syncwarp();
   float sk[2][GR], mk[2][GR], sv[2][GR], mv[2][GR];  // of keys kap and kap + 8
@@ -418,6 +442,20 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
     } else {
       const float2 x = lds_f2(scratch + (kap + 8 * hf) * 8), y = lds_f2(scratch + (16 + kap + 8 * hf) * 8);
       sk[hf][0] = x.x; mk[hf][0] = x.y; sv[hf][0] = y.x; mv[hf][0] = y.y;
+    }
+  }
+
+  // lane t's values: four keys, two words (d = 128: one of each group) of 8 channels at 8 g
+  uint32_t v[4][GR];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = 4 * i + ((i & 1) ? (t ^ 1) : t);
+    const uint32_t at = vc + (row0 + key) * Lay::CW + g * (4 * GR);
+    if constexpr (GR == 2) {
+      const uint2 y = lds64(at);
+      v[i][0] = y.x; v[i][1] = y.y;
+    } else {
+      v[i][0] = lds32(at);
     }
   }
 
@@ -527,19 +565,7 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
     }
   }
 
-  // O^T += V^T P^T: lane t's keys, two words (d = 128: one of each group) of 8 channels at 8 g
-  uint32_t v[4][GR];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = 4 * i + ((i & 1) ? (t ^ 1) : t);
-    const uint32_t at = vc + (row0 + key) * Lay::CW + g * (4 * GR);
-    if constexpr (GR == 2) {
-      const uint2 y = lds64(at);
-      v[i][0] = y.x; v[i][1] = y.y;
-    } else {
-      v[i][0] = lds32(at);
-    }
-  }
+  // O^T += V^T P^T
 #pragma unroll
   for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
@@ -580,7 +606,7 @@ template <int D, int NT, bool F32>
 __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, Ctl* ctl,
                                             float* buf, bool whole, float* slot, int warp, int lane) {
   using S = State<D, NT, F32>;
-  using Lay = Layout<D, NT>;
+  using Lay = Layout<D, NT, F32>;
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   const int g = lane >> 2, t = lane & 3;
   settle(st);
@@ -652,9 +678,9 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
 }
 
 // Fetch the next tile of this CTA's range into its stage (one thread at a time, in order).
-template <int D, int NT>
+template <int D, int NT, bool F32>
 __device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Ctl* ctl, uint32_t ring, int end) {
-  using Lay = Layout<D, NT>;
+  using Lay = Layout<D, NT, F32>;
   while (ctl->left == 0) {
     const int t = ctl->next;
     if (t >= end) return;
@@ -686,7 +712,7 @@ __device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Ctl* ctl, uint3
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
-  using Lay = Layout<D, NT>;
+  using Lay = Layout<D, NT, F32>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Ctl ctl;
   constexpr int STAGES = Lay::STAGES;
@@ -710,9 +736,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   const uint32_t ring = smem_u32(smem);
   if (tid == 0) {
     ctl.next = begin;
-    for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT>(a, &ctl, ring, end);
+    for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT, F32>(a, &ctl, ring, end);
   }
-  const uint32_t scratch = ring + STAGES * Lay::STAGE + warp * 512;
+  const uint32_t scratch = ring + Lay::AT_MERGE + warp * 512;
   int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
   uint32_t phase = 0;
   bool ok = true;
@@ -727,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
       left = min(min(u.tiles - u.tile0, end - t), (keys - key0 + kTile - 1) / kTile);  // (no keys: no tile to read)
       n0 = keys - a.nq + 1;  // keys that query position 0 attends
       rb = u.rb;
-      load_queries<D, NT, F32>(st, a, u, lane);
+      load_queries<D, NT, F32>(st, a, u, ring + Lay::AT_Q, warp == 0, lane);
     }
+    __syncthreads();
     key0 += 16 * warp;
     for (; left > 0; --left, key0 += kTile) {
       ok = ok && tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err);
@@ -736,9 +763,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
         const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
                        vs = ks + kTile * Lay::SW;
         if (key0 + 16 <= n0) {
-          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
+          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
         } else if (key0 < n0 + a.nq - 1) {
-          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows, lane);
+          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows, lane);
         }
         // The warps take turns to fetch: into the stage of the tile before this one, which the others
         // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
@@ -748,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
           if (turn == warp) {
             const int before = stage == 0 ? STAGES - 1 : stage - 1;
             if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
-              fetch_tile<D, NT>(a, &ctl, ring, end);
+              fetch_tile<D, NT, F32>(a, &ctl, ring, end);
           }
           tc::mbar_arrive(&ctl.empty[stage]);
         }
@@ -766,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     const bool whole = n == u.tiles;
     float* slot = nullptr;
     if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(Lay::ROWS);
-    finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + STAGES * Lay::STAGE), whole, slot, warp,
+    finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + Lay::AT_MERGE), whole, slot, warp,
                             lane);
     t += n;
   }
@@ -854,7 +881,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int
 
 template <int D, int NT, bool F32>
 cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
-  using Lay = Layout<D, NT>;
+  using Lay = Layout<D, NT, F32>;
   auto* kern = kv4_attn_kernel<D, NT, F32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::BYTES);
   if (e != cudaSuccess) return e;
