@@ -586,8 +586,6 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
     }
 }
 
-__device__ __forceinline__ void compute_sync() { __syncthreads(); }
-
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float4 v) {
   if constexpr (sizeof(T) == 4) {
@@ -601,16 +599,18 @@ __device__ __forceinline__ void store4(T* p, float4 v) {
 template <int D>
 __host__ __device__ constexpr int64_t slot_floats(int rows) { return (int64_t)rows * (D + 2); }
 
-// Merge the warps' states of one unit and write the output (`whole`) or the partial slot.
+// Merge the warps' states of one unit and write the output (`whole`) or the partial slot.  False,
+// to every thread, once a wait has given up: nothing is written then.
 template <int D, int NT, bool F32>
-__device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, Ctl* ctl,
+__device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4AttnArgs& a, const Unit& u, Ctl* ctl,
                                             float* buf, bool whole, float* slot, int warp, int lane) {
   using S = State<D, NT, F32>;
   using Lay = Layout<D, NT, F32>;
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   const int g = lane >> 2, t = lane & 3;
   settle(st);
-  compute_sync();  // (the merge buffer's first bytes were the loop's scratch)
+  // (the merge buffer's first bytes were the loop's scratch)
+  if (__syncthreads_or(ctl->abort)) return false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -630,7 +630,7 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
         ctl->l[warp][nt * 8 + 2 * t + e] = st.l[nt][e];
       }
     }
-  compute_sync();
+  __syncthreads();
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -649,7 +649,7 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
               make_float4(st.o[nt][gr * 4 + 2 * i][e] * f, st.o[nt][gr * 4 + 2 * i][2 + e] * f,
                           st.o[nt][gr * 4 + 2 * i + 1][e] * f, st.o[nt][gr * 4 + 2 * i + 1][2 + e] * f);
     }
-  compute_sync();
+  __syncthreads();
   for (int i = warp * 32 + lane; i < Lay::ROWS * (D / 4); i += kWarps * 32) {
     const int n = i / (D / 4), c = (i - n * (D / 4)) * 4;
     const int r = u.rb * Lay::ROWS + n;
@@ -674,7 +674,8 @@ __device__ __forceinline__ void finish_unit(State<D, NT, F32>& st, const Kv4Attn
       if (c == 0) *reinterpret_cast<float2*>(slot + Lay::ROWS * D + 2 * n) = make_float2(top, l);
     }
   }
-  compute_sync();  // the buffers are free for the next unit
+  __syncthreads();  // the buffers are free for the next unit
+  return true;
 }
 
 // Fetch the next tile of this CTA's range into its stage (one thread at a time, in order).
@@ -741,7 +742,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   const uint32_t scratch = ring + Lay::AT_MERGE + warp * 512;
   int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
   uint32_t phase = 0;
-  bool ok = true;
   for (int t = begin; t < end;) {
     State<D, NT, F32> st;
     int key0, n0, left, rb;
@@ -758,34 +758,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     __syncthreads();
     key0 += 16 * warp;
     for (; left > 0; --left, key0 += kTile) {
-      ok = ok && tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err);
-      if (ok) {
-        const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
-                       vs = ks + kTile * Lay::SW;
-        if (key0 + 16 <= n0) {
-          attend16<D, NT, F32, false>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
-        } else if (key0 < n0 + a.nq - 1) {
-          attend16<D, NT, F32, true>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows, lane);
-        }
-        // The warps take turns to fetch: into the stage of the tile before this one, which the others
-        // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
-        // happen one at a time and in order.
-        __syncwarp();
-        if (lane == 0) {
-          if (turn == warp) {
-            const int before = stage == 0 ? STAGES - 1 : stage - 1;
-            if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
-              fetch_tile<D, NT, F32>(a, &ctl, ring, end);
-          }
-          tc::mbar_arrive(&ctl.empty[stage]);
-        }
-        __syncwarp();
-        turn = (turn + 1) & (kWarps - 1);
+      if (!tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err)) break;
+      const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
+                     vs = ks + kTile * Lay::SW;
+      if (key0 + 16 <= n0) {
+        attend16<D, NT, F32, false>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
+      } else if (key0 < n0 + a.nq - 1) {
+        attend16<D, NT, F32, true>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows,
+                                   lane);
       }
+      // The warps take turns to fetch: into the stage of the tile before this one, which the others
+      // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
+      // happen one at a time and in order.
+      __syncwarp();
+      if (lane == 0) {
+        if (turn == warp) {
+          const int before = stage == 0 ? STAGES - 1 : stage - 1;
+          if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
+            fetch_tile<D, NT, F32>(a, &ctl, ring, end);
+        }
+        tc::mbar_arrive(&ctl.empty[stage]);
+      }
+      __syncwarp();
+      turn = (turn + 1) & (kWarps - 1);
+      if (turn == 0) settle(st);
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1;
-        settle(st);
       }
     }
     const Unit u = locate(a, ctl.cum, t);
@@ -793,8 +792,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     const bool whole = n == u.tiles;
     float* slot = nullptr;
     if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(Lay::ROWS);
-    finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + Lay::AT_MERGE), whole, slot, warp,
-                            lane);
+    if (!finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + Lay::AT_MERGE), whole, slot, warp,
+                                 lane))
+      break;
     t += n;
   }
   if (ctl.abort && tid == 0) {  // the copies in flight land in this CTA's shared memory: wait for them
