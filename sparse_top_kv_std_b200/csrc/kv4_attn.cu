@@ -342,22 +342,37 @@ __device__ __forceinline__ void settle(State<D, NT, F32>& st) {
     }
 }
 
-// 16 keys: rows [row0, row0 + 16) of the tile at shared addresses kc / vc / ks / vs, key0 = the
-// first one's position.  scratch: 512 bytes of this warp's.  MASK: some of the keys may lie past a
-// row's limit, n0 for query position 0 (or past the cache, where the shared memory holds stale bytes:
-// codes are finite whatever they are, scales are not).
+// A lane's byte offsets into shared memory: everything it reads of a warp's 16 rows lies at one of
+// them plus the stage's base plus a constant.
+template <int D, int NT, bool F32>
+struct LaneAt {
+  uint32_t k, v, scale, w16, r16;
+  __device__ __forceinline__ LaneAt(int warp, int lane) {
+    using Lay = Layout<D, NT, F32>;
+    const int g = lane >> 2, t = lane & 3;
+    const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);
+    k = (16 * warp + kap) * Lay::CW + t * (Lay::CW / 4);
+    v = kTile * Lay::CW + (16 * warp + t) * Lay::CW + g * (Lay::CW / 8);
+    scale = 2 * kTile * Lay::CW + (lane < 16 ? 0 : kTile * Lay::SW) + (16 * warp + (lane & 15)) * Lay::SW;
+    w16 = Lay::AT_MERGE + warp * 512 + lane * (2 * Lay::SW);
+    r16 = Lay::AT_MERGE + warp * 512 + kap * (2 * Lay::SW);
+  }
+};
+
+// A warp's 16 keys of the tile at shared address `tile` (of the ring at `ring`); key0 = the first
+// one's position.  MASK: some of the keys may lie past a row's limit, n0 for query position 0 (or past
+// the cache, where the shared memory holds stale bytes: codes are finite whatever they are, scales
+// are not).
 template <int D, int NT, bool F32, bool MASK>
-__device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uint32_t vc, uint32_t ks, uint32_t vs,
-                                         uint32_t qs, uint32_t scratch, int row0, int key0, int n0, int rb, int nq, int rows,
-                                         int lane) {
+__device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, NT, F32>& at, uint32_t ring,
+                                         uint32_t tile, int key0, int n0, int rb, int nq, int rows, int lane) {
   using S = State<D, NT, F32>;
   using Lay = Layout<D, NT, F32>;
   constexpr int GR = S::GR, WPL = D / 32;
-  const int g = lane >> 2, t = lane & 3;
-  const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);  // key of accumulator row g; row g + 8 is 8 higher
-
-  int lim[NT][2];  // keys the row attends
+  int lim[NT][2], kap = 0;  // keys a row attends; key of accumulator row lane / 4
   if constexpr (MASK) {
+    const int g = lane >> 2, t = lane & 3;
+    kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -369,17 +384,15 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
   // The 16 keys' scales to fp32, one half-warp for K and one for V, (s, m) of both groups: each lane
   // needs two keys' of each, and four lanes the same ones.
   {
-    const uint32_t at = (lane < 16 ? ks : vs) + (row0 + (lane & 15)) * Lay::SW;
     const float c = lane < 16 ? 0.f : 8.f, f = lane < 16 ? st.back : 1.f;
     if constexpr (GR == 2) {
-      const uint2 u = lds64(at);
+      const uint2 u = lds64(at.scale + tile);
       const float s0 = lo_bf16(u.x), s1 = lo_bf16(u.y);
-      sts_f4(scratch + lane * 16,
-             make_float4(f * s0, f * s1, f * fmaf(c, s0, hi_bf16(u.x)), f * fmaf(c, s1, hi_bf16(u.y))));
+      sts_f4(at.w16 + ring, make_float4(f * s0, f * s1, f * fmaf(c, s0, hi_bf16(u.x)), f * fmaf(c, s1, hi_bf16(u.y))));
     } else {
-      const uint32_t u = lds32(at);
+      const uint32_t u = lds32(at.scale + tile);
       const float s0 = lo_bf16(u);
-      sts_f2(scratch + lane * 8, make_float2(f * s0, f * fmaf(c, s0, hi_bf16(u))));
+      sts_f2(at.w16 + ring, make_float2(f * s0, f * fmaf(c, s0, hi_bf16(u))));
     }
   }
 
@@ -387,7 +400,7 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
   float acc[NT][GR][4];
   uint32_t wa[WPL], wb[WPL];
   {
-    const uint32_t ra = kc + (row0 + kap) * Lay::CW + t * (WPL * 4), rb = ra + 8 * Lay::CW;
+    const uint32_t ra = at.k + tile, rb = ra + 8 * Lay::CW;
     if constexpr (WPL == 4) {
       const uint4 x = lds128(ra), y = lds128(rb);
       wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
@@ -406,8 +419,8 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
     uint4 qh[NT], ql[F32 ? NT : 1];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      qh[nt] = lds128(qs + ((nt * WPL + w) * 32 + lane) * 16);
-      if constexpr (F32) ql[nt] = lds128(qs + (((NT + nt) * WPL + w) * 32 + lane) * 16);
+      qh[nt] = lds128(lane * 16 + (ring + Lay::AT_Q + (nt * WPL + w) * 512));
+      if constexpr (F32) ql[nt] = lds128(lane * 16 + (ring + Lay::AT_Q + ((NT + nt) * WPL + w) * 512));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -436,26 +449,30 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, uint32_t kc, uin
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     if constexpr (GR == 2) {
-      const float4 x = lds_f4(scratch + (kap + 8 * hf) * 16), y = lds_f4(scratch + (16 + kap + 8 * hf) * 16);
+      const float4 x = lds_f4(at.r16 + (ring + 128 * hf)), y = lds_f4(at.r16 + (ring + 128 * hf + 256));
       sk[hf][0] = x.x; sk[hf][1] = x.y; mk[hf][0] = x.z; mk[hf][1] = x.w;
       sv[hf][0] = y.x; sv[hf][1] = y.y; mv[hf][0] = y.z; mv[hf][1] = y.w;
     } else {
-      const float2 x = lds_f2(scratch + (kap + 8 * hf) * 8), y = lds_f2(scratch + (16 + kap + 8 * hf) * 8);
+      const float2 x = lds_f2(at.r16 + (ring + 64 * hf)), y = lds_f2(at.r16 + (ring + 64 * hf + 128));
       sk[hf][0] = x.x; mk[hf][0] = x.y; sv[hf][0] = y.x; mv[hf][0] = y.y;
     }
   }
 
-  // lane t's values: four keys, two words (d = 128: one of each group) of 8 channels at 8 g
+  // lane t's values: four keys (t, 4 + (t ^ 1), ...), two words (d = 128: one of each group) of 8
+  // channels at 8 g.  A row is CW bytes and the rows of a warp start at a multiple of 4 CW, so t ^ 1
+  // is one bit of the address.
   uint32_t v[4][GR];
+  {
+    const uint32_t even = at.v + tile, odd = even ^ Lay::CW;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = 4 * i + ((i & 1) ? (t ^ 1) : t);
-    const uint32_t at = vc + (row0 + key) * Lay::CW + g * (4 * GR);
-    if constexpr (GR == 2) {
-      const uint2 y = lds64(at);
-      v[i][0] = y.x; v[i][1] = y.y;
-    } else {
-      v[i][0] = lds32(at);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = ((i & 1) ? odd : even) + 4 * i * Lay::CW;
+      if constexpr (GR == 2) {
+        const uint2 y = lds64(row);
+        v[i][0] = y.x; v[i][1] = y.y;
+      } else {
+        v[i][0] = lds32(row);
+      }
     }
   }
 
@@ -717,7 +734,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Ctl ctl;
   constexpr int STAGES = Lay::STAGES;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same for the warp)
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&ctl.full[s], 1);
@@ -739,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     ctl.next = begin;
     for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT, F32>(a, &ctl, ring, end);
   }
-  const uint32_t scratch = ring + Lay::AT_MERGE + warp * 512;
+  const LaneAt<D, NT, F32> at(warp, lane);
   int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
   uint32_t phase = 0;
   for (int t = begin; t < end;) {
@@ -759,13 +777,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     key0 += 16 * warp;
     for (; left > 0; --left, key0 += kTile) {
       if (!tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err)) break;
-      const uint32_t kc = ring + stage * Lay::STAGE, vc = kc + kTile * Lay::CW, ks = vc + kTile * Lay::CW,
-                     vs = ks + kTile * Lay::SW;
+      const uint32_t tile = ring + stage * Lay::STAGE;
       if (key0 + 16 <= n0) {
-        attend16<D, NT, F32, false>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, 0, 0, 0, 1, 0, lane);
+        attend16<D, NT, F32, false>(st, at, ring, tile, 0, 0, 0, 1, 0, lane);
       } else if (key0 < n0 + a.nq - 1) {
-        attend16<D, NT, F32, true>(st, kc, vc, ks, vs, ring + Lay::AT_Q, scratch, 16 * warp, key0, n0, rb, a.nq, a.rows,
-                                   lane);
+        attend16<D, NT, F32, true>(st, at, ring, tile, key0, n0, rb, a.nq, a.rows, lane);
       }
       // The warps take turns to fetch: into the stage of the tile before this one, which the others
       // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
