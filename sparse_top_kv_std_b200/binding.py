@@ -167,10 +167,22 @@ def _nbytes(x) -> int:
     return 0 if x is None else x.numel() * x.element_size()
 
 
+_raw_stream = None  # the current stream's handle, without a Stream object for every call
+
+
+def _current_stream() -> int:
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # initialises CUDA, or raises
+        handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _raw_stream = lambda: handle(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -392,18 +404,44 @@ def std_rope(inv_freq, sections=None, interleaved=False) -> StdRope:
     return r
 
 
-def _tokens(x, dims, heads):
+def _current_device() -> int:
+    global _device
+    if _device is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA, or raises
+        _device = torch._C._cuda_getDevice
+    return _device()
+
+
+_device = None
+
+
+def _on(x, dev) -> Optional[int]:
+    """Pointer of a contiguous tensor on device `dev`, the one the call runs on."""
+    if x is None:
+        return None
+    if x.get_device() != dev:
+        raise ValueError("expected a CUDA tensor on the current device")
+    if not x.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return x.data_ptr()
+
+
+def _tokens(x, L, nB, heads, d, dev):
     """Pointer and token stride of a projection output [L][B][rows][heads][d], which may be a view of
     a fused one (any token stride)."""
     if x is None:
         return None, 0
-    if not x.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if x.dim() != 5 or tuple(x.shape[:2]) != (dims.L, dims.B) or tuple(x.shape[3:]) != (heads, dims.d):
-        raise ValueError(f"expected [L][B][rows][{heads}][{dims.d}], got {tuple(x.shape)}")
-    s = x.stride(2) if x.shape[2] > 1 else x.stride(1) if x.shape[1] > 1 else x.stride(0) if x.shape[0] > 1 else heads * dims.d
-    want = (x.shape[1] * x.shape[2] * s, x.shape[2] * s, s, dims.d, 1)
-    if any(n > 1 and a != b for n, a, b in zip(x.shape, x.stride(), want)):
+    if x.get_device() != dev:
+        raise ValueError("expected a CUDA tensor on the current device")
+    shape = x.shape
+    if len(shape) != 5 or shape[0] != L or shape[1] != nB or shape[3] != heads or shape[4] != d:
+        raise ValueError(f"expected [{L}][{nB}][rows][{heads}][{d}], got {tuple(shape)}")
+    s0, s1, s, s3, s4 = x.stride()
+    rows = shape[2]
+    if rows == 1:
+        s = s1 if nB > 1 else s0 if L > 1 else heads * d
+    if s4 != 1 or (heads > 1 and s3 != d) or (nB > 1 and s1 != rows * s) or (L > 1 and s0 != nB * rows * s):
         raise ValueError("tokens must be evenly spaced and a token's heads contiguous")
     return x.data_ptr(), s
 
@@ -411,33 +449,40 @@ def _tokens(x, dims, heads):
 def std_qk_norm_rope(d: StdDims, rope: StdRope, q_in, k_in, v_in, rows, n_rows, q_weight, k_weight, eps, pos, q_out,
                      k_cache, v_cache, cap, length, pos_offset=0, stream=None) -> None:
     """q_in / k_in / v_in: [L][B][rows][heads][d] tensors or views of a fused projection's output (or None)."""
-    q, qs = _tokens(q_in, d, d.Hq)
-    k, ks = _tokens(k_in, d, d.Hkv)
-    v, vs = _tokens(v_in, d, d.Hkv)
-    _check(lib().std_qk_norm_rope(ctypes.byref(d), ctypes.byref(rope), q, qs, k, ks, v, vs, rows, _ptr(n_rows),
-                                  _ptr(q_weight), _ptr(k_weight), eps, _ptr(pos), _ptr(q_out), _ptr(k_cache),
-                                  _ptr(v_cache), cap, _ptr(length), pos_offset, _stream(stream)))
+    dev = _current_device()
+    L, nB, Hkv, hd = d.L, d.B, d.Hkv, d.d
+    q, qs = _tokens(q_in, L, nB, d.Hq, hd, dev)
+    k, ks = _tokens(k_in, L, nB, Hkv, hd, dev)
+    v, vs = _tokens(v_in, L, nB, Hkv, hd, dev)
+    _check(lib().std_qk_norm_rope(ctypes.byref(d), ctypes.byref(rope), q, qs, k, ks, v, vs, rows, _on(n_rows, dev),
+                                  _on(q_weight, dev), _on(k_weight, dev), eps, _on(pos, dev), _on(q_out, dev),
+                                  _on(k_cache, dev), _on(v_cache, dev), cap, _on(length, dev), pos_offset,
+                                  _stream(stream)))
 
 
 # 4-bit cache: a dict with the std_kv4_cache field names (four tensors and cap), see kv4.Kv4Cache
 
-def _kv4(cache) -> StdKv4Cache:
-    return StdKv4Cache(*[_ptr(cache[f]) for f, _ in StdKv4Cache._fields_])
+def _kv4(c, dev):
+    return ctypes.byref(StdKv4Cache(_on(c["k_codes"], dev), _on(c["k_scales"], dev), _on(c["v_codes"], dev),
+                                    _on(c["v_scales"], dev), c["cap"]))
 
 
 def std_kv4_append(d: StdDims, cache: dict, length, pos_offset, k_new, v_new, n_new, stream=None) -> None:
-    _check(lib().std_kv4_append(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(length), pos_offset, _ptr(k_new),
-                                _ptr(v_new), n_new, _stream(stream)))
+    dev = _current_device()
+    _check(lib().std_kv4_append(ctypes.byref(d), _kv4(cache, dev), _on(length, dev), pos_offset, _on(k_new, dev),
+                                _on(v_new, dev), n_new, _stream(stream)))
 
 
 def std_kv4_quantize(d: StdDims, cache: dict, k_full, v_full, begin, count, max_n, stream=None) -> None:
-    _check(lib().std_kv4_quantize(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(k_full), _ptr(v_full), _ptr(begin),
-                                  _ptr(count), max_n, _stream(stream)))
+    dev = _current_device()
+    _check(lib().std_kv4_quantize(ctypes.byref(d), _kv4(cache, dev), _on(k_full, dev), _on(v_full, dev), _on(begin, dev),
+                                  _on(count, dev), max_n, _stream(stream)))
 
 
 def std_kv4_read(d: StdDims, cache: dict, begin, count, max_n, k_out, v_out, stream=None) -> None:
-    _check(lib().std_kv4_read(ctypes.byref(d), ctypes.byref(_kv4(cache)), _ptr(begin), _ptr(count), max_n, _ptr(k_out),
-                              _ptr(v_out), _stream(stream)))
+    dev = _current_device()
+    _check(lib().std_kv4_read(ctypes.byref(d), _kv4(cache, dev), _on(begin, dev), _on(count, dev), max_n,
+                              _on(k_out, dev), _on(v_out, dev), _stream(stream)))
 
 
 def std_kv4_attn_workspace_size(d: StdDims, q_rows: int, cap: int) -> int:
@@ -445,8 +490,9 @@ def std_kv4_attn_workspace_size(d: StdDims, q_rows: int, cap: int) -> int:
 
 
 def std_kv4_attn(d: StdDims, q, q_rows, cache: dict, length, len_offset, o, ws, stream=None) -> None:
-    _check(lib().std_kv4_attn(ctypes.byref(d), _ptr(q), q_rows, ctypes.byref(_kv4(cache)), _ptr(length), len_offset,
-                              _ptr(o), _ptr(ws), _nbytes(ws), _stream(stream)))
+    dev = _current_device()
+    _check(lib().std_kv4_attn(ctypes.byref(d), _on(q, dev), q_rows, _kv4(cache, dev), _on(length, dev), len_offset,
+                              _on(o, dev), _on(ws, dev), _nbytes(ws), _stream(stream)))
 
 
 def std_kv_commit(d: StdDims, k_full, v_full, k_sparse, v_sparse, len_full, len_sparse, n_plus_1, max_n,

@@ -33,6 +33,9 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+#include <type_traits>
+
 namespace stdb {
 namespace {
 
@@ -411,8 +414,6 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
       wb[0] = y.x; wb[1] = y.y;
     }
   }
-  // (two chains of products for each partial sum: half the latency)
-  float acc2[NT][GR][4];
 #pragma unroll
   for (int w = 0; w < WPL; ++w) {
     const int gr = GR == 2 ? (w & 1) : 0;
@@ -428,8 +429,8 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
       const uint32_t a0 = widen0(x), a1 = widen0(y), a2 = widen4(x), a3 = widen4(y);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float(&c)[4] = k ? acc2[nt][gr] : acc[nt][gr];
-        if (w < GR)
+        float(&c)[4] = acc[nt][gr];
+        if (w < GR && k == 0)
           mma_f16_zero(c, a0, a1, a2, a3, k ? qh[nt].z : qh[nt].x, k ? qh[nt].w : qh[nt].y);
         else
           mma_f16(c, a0, a1, a2, a3, k ? qh[nt].z : qh[nt].x, k ? qh[nt].w : qh[nt].y);
@@ -437,12 +438,6 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
       }
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][gr][i] += acc2[nt][gr][i];
 
   __syncwarp();
   float sk[2][GR], mk[2][GR], sv[2][GR], mv[2][GR];  // of keys kap and kap + 8
@@ -455,24 +450,6 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
     } else {
       const float2 x = lds_f2(at.r16 + (ring + 64 * hf)), y = lds_f2(at.r16 + (ring + 64 * hf + 128));
       sk[hf][0] = x.x; mk[hf][0] = x.y; sv[hf][0] = y.x; mv[hf][0] = y.y;
-    }
-  }
-
-  // lane t's values: four keys (t, 4 + (t ^ 1), ...), two words (d = 128: one of each group) of 8
-  // channels at 8 g.  A row is CW bytes and the rows of a warp start at a multiple of 4 CW, so t ^ 1
-  // is one bit of the address.
-  uint32_t v[4][GR];
-  {
-    const uint32_t even = at.v + tile, odd = even ^ Lay::CW;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = ((i & 1) ? odd : even) + 4 * i * Lay::CW;
-      if constexpr (GR == 2) {
-        const uint2 y = lds64(row);
-        v[i][0] = y.x; v[i][1] = y.y;
-      } else {
-        v[i][0] = lds32(row);
-      }
     }
   }
 
@@ -582,7 +559,23 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
     }
   }
 
-  // O^T += V^T P^T
+  // O^T += V^T P^T with lane t's values: four keys (t, 4 + (t ^ 1), ...), two words (d = 128: one of each group) of 8
+  // channels at 8 g.  A row is CW bytes and the rows of a warp start at a multiple of 4 CW, so t ^ 1
+  // is one bit of the address.
+  uint32_t v[4][GR];
+  {
+    const uint32_t even = at.v + tile, odd = even ^ Lay::CW;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = ((i & 1) ? odd : even) + 4 * i * Lay::CW;
+      if constexpr (GR == 2) {
+        const uint2 y = lds64(row);
+        v[i][0] = y.x; v[i][1] = y.y;
+      } else {
+        v[i][0] = lds32(row);
+      }
+    }
+  }
 #pragma unroll
   for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
@@ -899,8 +892,15 @@ template <int D, int NT, bool F32>
 cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
   using Lay = Layout<D, NT, F32>;
   auto* kern = kv4_attn_kernel<D, NT, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::BYTES);
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev > 63 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
   e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), Lay::BYTES, s, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.L * a.B * a.Hkv * a.rows;

@@ -187,8 +187,13 @@ def test_workspace_of_invalid_arguments_is_zero():
 
 def test_binding_refuses_uneven_token_views():
     torch = pytest.importorskip("torch")
-    d = B.dims(1, 2, 4, 2, 64, B.STD_F32, 16, 1)
     with pytest.raises(ValueError):
-        B._tokens(torch.zeros(1, 2, 3, 4, 64), d, 4)             # not on the GPU
+        B._tokens(torch.zeros(1, 2, 3, 4, 64), 1, 2, 4, 64, 0)   # not on the GPU
+    for view in (torch.zeros(1, 2, 3, 4, 64), torch.zeros(1, 2, 3, 6, 64)[:, :, :, 1:5], torch.zeros(1, 2, 1, 9, 64)[:, :, :, :4]):
+        assert B._tokens(view, 1, 2, 4, 64, -1)[1] == view.stride(2) or view.shape[2] == 1
+    for view in (torch.zeros(1, 2, 5, 4, 64)[:, :, :3], torch.zeros(1, 2, 3, 4, 128)[..., :64], torch.zeros(1, 2, 3, 64, 4).mT,
+                 torch.zeros(1, 2, 4, 3, 64).transpose(2, 3), torch.zeros(2, 3, 4, 64), torch.zeros(1, 2, 3, 5, 64)):
+        with pytest.raises(ValueError):
+            B._tokens(view, 1, 2, 4, 64, -1)
     with pytest.raises(ValueError):
         B.std_rope(torch.zeros(32), sections=[32])               # not float64
