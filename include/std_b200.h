@@ -538,7 +538,7 @@ int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_i
  * dense decoding.
  *
  * A row is d / 64 groups of 64 channels (d = 64 or 128), each with a bfloat16 scale s and minimum m:
- *   m = bf16(min x),  s = bf16(float(max x - m) / 15),  c = clamp(round(float(x - m) / s), 0, 15)
+ *   m = bf16(min x),  s = bf16(max(float(max x - m), 0) / 15),  c = clamp(round(float(x - m) / s), 0, 15)
  * (ties to even; the quotient is rounded as if it were exact), and code c stands for m + c s.  A group
  * with an infinity or a NaN, or wider than fp32 can hold, reads back as NaN in all its channels; one
  * whose s is 0 reads back as m.

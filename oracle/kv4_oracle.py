@@ -45,7 +45,7 @@ def kv4_quantize(x: np.ndarray) -> Tuple[np.ndarray, np.ndarray, np.ndarray]:
     with np.errstate(all="ignore"):
         m = bf16_round(g.min(-1))
         span = g.max(-1) - m
-        s = bf16_round(span / np.float32(15))
+        s = bf16_round(np.maximum(span, 0) / np.float32(15))  # (fp32 input: m may round above max x)
         diff = (g - m[..., None]).astype(np.float64)
         c = np.clip(np.round(diff / s[..., None].astype(np.float64)), 0, 15)
     bad = ~np.isfinite(span)

@@ -7,9 +7,11 @@
 // NaN gets m = NaN, s = 0: all its channels read back as NaN.  A group whose range is too
 // small for a bf16 scale gets s = 0 and reads back as m.
 //
-// Both directions stream: 2 d values in, d + d / 8 bytes out for the K and V row of a head.
-// A lane holds one code word (8 channels), so the codes of a row are one coalesced store, and a
-// group's extremes are three shuffles over its eight lanes.
+// Both directions stream: 2 d values in, d + d / 8 bytes out for the K and V row of a head, and the
+// instructions on the way are what is hard to hide: at full HBM rate an SM has about 13 issue slots
+// for a bf16 channel.  When writing a lane holds 16 channels of a group (four lanes a group: two
+// shuffles for each extreme, and a group's scale is worked out four times, not eight), and a code
+// is nine float or integer instructions without a division, a conversion or a branch (code_word).
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -20,14 +22,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows a lane group has in flight
 
-__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if either is
+__device__ __forceinline__ float min_nan(float a, float b, float c) {  // NaN if one is
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -58,15 +60,42 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
-// The code of one channel: diff / s rounded half to even, exactly.  `k` is within one of the
-// answer; diff - k s is exact in fp32 next to a border (k s has at most 12 bits, and both
-// terms are multiples of the smaller one's last bit, at most 24 bits apart).
-__device__ __forceinline__ float settle(float k, float diff, float s) {
-  const float r = fmaf(-k, s, diff), h = 0.5f * s;
-  const bool odd = ((int)k & 1) != 0;
-  if (r > h || (r == h && odd)) k += 1.f;
-  else if (r < -h || (r == -h && odd)) k -= 1.f;
-  return k;
+// Codes of 8 channels x - m >= 0, as one word.  c = floor(q) + (the rest is at least a half), q =
+// diff / s.  floor: adding 1.5 2^23 to diff / s with rounding down leaves it in the last bits; 1 / s is
+// good to 2^-23, so the floor is right except within 2^-19 of an integer, and there the comparison
+// below comes out the same from either side.  rest: diff - floor s is exact (floor s has 12 bits, and
+// its last bit and diff's are within 24 of the larger one); it counts as a half or more from s / 2 on
+// where the floor is odd and above s / 2 where it is even, and the bit pattern of s / 2 is even (s has
+// 8 bits), so "above" is one more in the last place.
+__device__ __forceinline__ uint32_t code_word(const float (&diff)[8], float s, float inv) {
+  const uint32_t half = __float_as_uint(0.5f * s);
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const float t = __fmaf_rd(diff[i], inv, 12582912.f);
+    const uint32_t tb = __float_as_uint(t);
+    const float rest = fmaf(12582912.f - t, s, diff[i]);
+    const float over = rest - __uint_as_float(half | (~tb & 1u));
+    word = word * 16 + (tb + (uint32_t)(__float_as_int(over) >> 31));  // floor, or floor - 1 when below
+  }
+  return word - 0x11111111u * 0x4b3fffffu;  // the bits of 1.5 2^23, less one, in every place
+}
+
+// The same for a scale so small that 1 / s or the products above leave the normal numbers: scaled up
+// by a power of two, quotients and remainders one at a time.
+__device__ __noinline__ uint32_t code_word_tiny(const float* diff, float s) {
+  const float up = 1.208925820e24f;  // 2^80
+  uint32_t word = 0;
+  for (int i = 7; i >= 0; --i) {
+    const float d = diff[i] * up, t = s * up;
+    float k = fminf(rintf(d / t), 16.f);
+    const float r = fmaf(-k, t, d), h = 0.5f * t;
+    const bool odd = ((int)k & 1) != 0;
+    if (r > h || (r == h && odd)) k += 1.f;
+    else if (r < -h || (r == -h && odd)) k -= 1.f;
+    word = (word << 4) | (uint32_t)fminf(fmaxf(k, 0.f), 15.f);
+  }
+  return word;
 }
 
 // Where the rows of one call come from and go to: rows r < count of sequence b.
@@ -83,8 +112,9 @@ __device__ __forceinline__ bool row_span(const Kv4Args& a, int b, RowSpan* sp) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, int chunks) {
-  constexpr int LPR = D / 8;               // lanes of a row
-  constexpr int RPB = kThreads / LPR;      // rows of a CTA at a time
+  constexpr int GR = D / kKv4Group;
+  constexpr int LPR = D / 16;          // lanes of a row: word pairs (2 j, 2 j + 1) of one group
+  constexpr int RPB = kThreads / LPR;  // rows of a CTA at a time
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
   const int which = blockIdx.x & 1;
@@ -99,63 +129,71 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, in
   const T* src = static_cast<const T*>(which ? a.v : a.k);
   uint32_t* codes = static_cast<uint32_t*>(which ? a.v_codes : a.k_codes);
   uint32_t* scales = static_cast<uint32_t*>(which ? a.v_scales : a.k_scales);
-  const int w = threadIdx.x % LPR, grp = D == 128 ? w & 1 : 0, j = D == 128 ? w >> 1 : w;
-  const int ch = kv4_word_channel<D>(w);
+  const int j = threadIdx.x % 4, grp = GR == 2 ? threadIdx.x / 4 % 2 : 0;
+  const int ch = 64 * grp + 16 * j;
   const int r0 = chunk * RPB * kUnroll + threadIdx.x / LPR;
-  float x[kUnroll][8];
+  if (r0 - threadIdx.x / LPR >= sp.n) return;
+  float x[kUnroll][2][8];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int r = r0 + u * RPB;
-    if (r < sp.n) {
-      load8<T>(src + ((int64_t)prob * a.rows_cap + (a.at_pos ? sp.pos : 0) + r) * D + ch, x[u]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-    }
+    const int r = min(r0 + u * RPB, sp.n - 1);  // (past the end: a row that is not stored)
+    const T* p = src + ((int64_t)prob * a.rows_cap + (a.at_pos ? sp.pos : 0) + r) * D + ch;
+    load8<T>(p, x[u][0]);
+    load8<T>(p + 8, x[u][1]);
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int r = r0 + u * RPB;
-    float lo = x[u][0], hi = x[u][0];
+    if ((r0 & ~(32 / LPR - 1)) + u * RPB >= sp.n) break;  // (none of the warp's rows)
+    float lo = x[u][0][0], hi = lo;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      lo = min_nan(lo, x[u][i]);
-      hi = max_nan(hi, x[u][i]);
+    for (int i = 1; i < 16; i += 2) {
+      const float y = x[u][i / 8][i % 8], z = x[u][(i + 1) / 8 % 2][(i + 1) % 8];  // (the last z is the first again)
+      lo = min_nan(lo, y, z);
+      hi = max_nan(hi, y, z);
     }
 #pragma unroll
-    for (int o = D == 128 ? 2 : 1; o < LPR; o <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    for (int o = 1; o < 4; o <<= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, lo, o), z = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo = min_nan(lo, lo, y);
+      hi = max_nan(hi, hi, z);
     }
-    __nv_bfloat16 mb = __float2bfloat16_rn(lo);
-    float m = __bfloat162float(mb);
+    const float m = __bfloat162float(__float2bfloat16_rn(lo));
     const float range = hi - m;
-    __nv_bfloat16 sb = __float2bfloat16_rn(range / 15.f);
-    float s = __bfloat162float(sb);
+    float s = __bfloat162float(__float2bfloat16_rn(range / 15.f));
     const bool finite = fabsf(range) <= 3.402823466e38f;  // false for a NaN or an infinity
-    uint32_t word = 0;
+    uint32_t w0 = 0, w1 = 0;
     if (finite && s > 0.f) {
-      // keep 1 / s finite for the smallest scales (exact: a power of two)
-      const float up = s < 5.421010862e-20f ? 1.208925820e24f : 1.f;  // 2^-64, 2^80
-      const float ss = s * up, inv = 1.f / ss;
 #pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        const float diff = (x[u][i] - m) * up;
-        float k = fminf(fmaxf(rintf(diff * inv), 0.f), 16.f);
-        k = settle(k, diff, ss);
-        word = (word << 4) | (uint32_t)fminf(fmaxf(k, 0.f), 15.f);
+      for (int i = 0; i < 16; ++i) {
+        const float d = x[u][i / 8][i % 8] - m;
+        x[u][i / 8][i % 8] = sizeof(T) == 4 ? fmaxf(d, 0.f) : d;  // (bf16: m is the smallest x)
+      }
+      if (s >= 7.888609052e-31f) {  // 2^-100
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        w0 = code_word(x[u][0], s, inv);
+        w1 = code_word(x[u][1], s, inv);
+      } else {
+        float y[16];  // (a copy: only this path's needs an address)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = x[u][i / 8][i % 8];
+        w0 = code_word_tiny(y, s);
+        w1 = code_word_tiny(y + 8, s);
       }
     } else {
       s = 0.f;
-      sb = __float2bfloat16_rn(0.f);
-      if (!finite) mb = __float2bfloat16_rn(__uint_as_float(0x7fc00000u));
     }
+    const int r = r0 + u * RPB;
     if (r < sp.n && STD_DCHECK(sp.pos + r < a.cap, a.err)) {
       const int64_t row = (int64_t)prob * a.cap + sp.pos + r;
-      codes[row * LPR + w] = word;
-      if (j == 0)
-        scales[row * (D / kKv4Group) + grp] =
-            (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
+      uint32_t* q = codes + row * (D / 8);
+      if constexpr (GR == 2) {
+        q[4 * j + grp] = w0;
+        q[4 * j + 2 + grp] = w1;
+      } else {
+        *reinterpret_cast<uint2*>(q + 2 * j) = make_uint2(w0, w1);
+      }
+      if (j == 0) scales[row * GR + grp] = (__float_as_uint(s) >> 16) | (finite ? __float_as_uint(m) : 0x7fc00000u);
     }
   }
 }
@@ -197,16 +235,21 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Args a, int
     const int r = r0 + u * RPB;
     if (r >= sp.n) break;
     const float s = __uint_as_float(sc[u] << 16), m = __uint_as_float(sc[u] & 0xffff0000u);
+    // 2^23 + c, one byte permutation, less 2^23
+    const uint32_t even = word[u] & 0x0f0f0f0fu, odd = (word[u] >> 4) & 0x0f0f0f0fu;
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf((float)((word[u] >> (4 * i)) & 15u), s, m);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t f = __byte_perm(i & 1 ? odd : even, 0x4b000000u, 0x7550 + i / 2);
+      x[i] = fmaf(__uint_as_float(f) - 8388608.f, s, m);
+    }
     store8<T>(dst + ((int64_t)prob * a.rows_cap + r) * D + ch, x);
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(const Kv4Args& a, bool read, cudaStream_t s) {
-  constexpr int per_cta = kThreads / (D / 8) * kUnroll;
+  const int per_cta = kThreads / (D / (read ? 8 : 16)) * kUnroll;
   const int chunks = (a.max_n + per_cta - 1) / per_cta;
   const dim3 grid((unsigned)(2 * (int64_t)a.L * a.B * a.Hkv * chunks));
   if (read) return launch_pdl(kv4_read_kernel<T, D>, grid, dim3(kThreads), 0, s, a, chunks);
