@@ -870,7 +870,7 @@ int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_i
   }
   if (sum != rope->rot_dim / 2)
     return fail(STD_ERR_INVALID_ARG, "the sections hold %d pairs, rot_dim / 2 = %d", sum, rope->rot_dim / 2);
-  // (the kernel numbers its CTAs in 31 bits: at most one for 16 heads of a token)
+  // (the kernel numbers its CTAs in 31 bits: one for a few tokens of a sequence at least)
   if ((int64_t)dims->L * dims->B * (rows / 4 + 1) > (1 << 30)) return fail(STD_ERR_INVALID_ARG, "too many tokens");
   int *err, sms;
   STD_TRY(device_state(&err, &sms));

@@ -33,21 +33,26 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   return r;
 }
 
+// 16 channels as they were read.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 u = __ldcs(reinterpret_cast<const float4*>(p)), v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-  } else {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw16 {
+  static constexpr int N = 4 * sizeof(T);  // 32-bit words
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
     }
   }
-}
+  __device__ __forceinline__ void get(float (&x)[2][8]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (sizeof(T) == 4) x[i / 8][i % 8] = __uint_as_float(w[i]);
+      else x[i / 8][i % 8] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
@@ -133,21 +138,21 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, in
   const int ch = 64 * grp + 16 * j;
   const int r0 = chunk * RPB * kUnroll + threadIdx.x / LPR;
   if (r0 - threadIdx.x / LPR >= sp.n) return;
-  float x[kUnroll][2][8];
+  Raw16<T> raw[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int r = min(r0 + u * RPB, sp.n - 1);  // (past the end: a row that is not stored)
-    const T* p = src + ((int64_t)prob * a.rows_cap + (a.at_pos ? sp.pos : 0) + r) * D + ch;
-    load8<T>(p, x[u][0]);
-    load8<T>(p + 8, x[u][1]);
+    raw[u].load(src + ((int64_t)prob * a.rows_cap + (a.at_pos ? sp.pos : 0) + r) * D + ch);
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     if ((r0 & ~(32 / LPR - 1)) + u * RPB >= sp.n) break;  // (none of the warp's rows)
-    float lo = x[u][0][0], hi = lo;
+    float x[2][8];
+    raw[u].get(x);
+    float lo = x[0][0], hi = lo;
 #pragma unroll
     for (int i = 1; i < 16; i += 2) {
-      const float y = x[u][i / 8][i % 8], z = x[u][(i + 1) / 8 % 2][(i + 1) % 8];  // (the last z is the first again)
+      const float y = x[i / 8][i % 8], z = x[(i + 1) / 8 % 2][(i + 1) % 8];  // (the last z is the first again)
       lo = min_nan(lo, y, z);
       hi = max_nan(hi, y, z);
     }
@@ -165,18 +170,18 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, in
     if (finite && s > 0.f) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float d = x[u][i / 8][i % 8] - m;
-        x[u][i / 8][i % 8] = sizeof(T) == 4 ? fmaxf(d, 0.f) : d;  // (bf16: m is the smallest x)
+        const float d = x[i / 8][i % 8] - m;
+        x[i / 8][i % 8] = sizeof(T) == 4 ? fmaxf(d, 0.f) : d;  // (bf16: m is the smallest x)
       }
       if (s >= 7.888609052e-31f) {  // 2^-100
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        w0 = code_word(x[u][0], s, inv);
-        w1 = code_word(x[u][1], s, inv);
+        w0 = code_word(x[0], s, inv);
+        w1 = code_word(x[1], s, inv);
       } else {
         float y[16];  // (a copy: only this path's needs an address)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = x[u][i / 8][i % 8];
+        for (int i = 0; i < 16; ++i) y[i] = x[i / 8][i % 8];
         w0 = code_word_tiny(y, s);
         w1 = code_word_tiny(y + 8, s);
       }

@@ -16,6 +16,8 @@
 #include "common.cuh"
 #include "internal.h"
 
+#include <type_traits>
+
 namespace stdb {
 namespace {
 
@@ -78,69 +80,106 @@ __device__ __forceinline__ void pack(const float (&x)[E], Vec<E * sizeof(T)>& v)
 
 constexpr int kBatch = 4;  // heads a half-warp has in flight
 
-// Heads [h0, h1) of one part (q, k or v) of one token, every `step`-th, by one half-warp: src and dst are
-// the token's head h0, a head apart by src_step / dst_step.  (c, s): cosines and signed sines of the
-// lane's channels.
+// What a half-warp does of one part (q, k or v) of its token: n heads, from src / dst on, a head apart
+// by d / dst_step.
+template <typename T>
+struct Part {
+  const T* src;
+  T* dst;
+  int64_t dst_step;
+  int n;
+  const T* w;  // weights of the norm, or NULL
+};
+
+template <typename T, int E>
+__device__ __forceinline__ void load_heads(Vec<E * sizeof(T)> (&v)[kBatch], const Part<T>& p, int h, int e0) {
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (h + i < p.n) v[i].load(p.src + (h + i) * (16 * E) + e0);
+}
+
+// The heads of one part, the first kBatch of them loaded.  Channel j of a lane becomes
+//   x_j (c_j w_j) inv + x_partner (s_j w_partner) inv
+// so the weights join the cosines and signed sines (c = 1, s = 0 past the rotated channels), once for
+// all heads, and the partner's value travels as it was read, two bf16 in a shuffle.
 template <typename T, int E, bool ROTATE>
-__device__ __forceinline__ void run_heads(const T* src, int64_t src_step, T* dst, int64_t dst_step, int n, const T* w,
-                                          float eps, const float (&c)[E], const float (&s)[E], int partner,
-                                          bool interleaved, uint32_t mask) {
+__device__ __forceinline__ void run_heads(Vec<E * sizeof(T)> (&v)[kBatch], const Part<T>& p, const float2* cs, int half,
+                                          bool interleaved, float eps, int e0, uint32_t mask) {
   constexpr int D = 16 * E;
   using V = Vec<E * sizeof(T)>;
-  float wf[E];
-  if (ROTATE && w) {
-    V v;
-    v.load(w);
-    unpack<T, E>(v, wf);
-  }
-  for (int h = 0; h < n; h += kBatch) {
-    V v[kBatch];
+  float c[E], s[E];
+  int partner = threadIdx.x & 31;
+  if constexpr (ROTATE) {
+    // (E divides half, so a lane lies wholly in the first half, the second, or past both)
+    const bool first = e0 < half, second = !first && e0 < 2 * half;
+    const int shift = interleaved ? 0 : first ? half : second ? -half : 0;  // channels to the partner's
+    partner += shift / E;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (h + i < n) v[i].load(src + (h + i) * src_step);
+    for (int j = 0; j < E; ++j) {
+      const int q = interleaved ? (e0 + j) >> 1 : first ? e0 + j : e0 - half + j;
+      const float2 f = first || second ? cs[q] : make_float2(1.f, 0.f);
+      c[j] = f.x;
+      s[j] = (interleaved ? !(j & 1) : first) ? -f.y : f.y;
+    }
+    if (p.w) {
+      V wv, wp;
+      wv.load(p.w + e0);
+      wp.load(p.w + e0 + shift);
+      float x[E], y[E];
+      unpack<T, E>(wv, x);
+      unpack<T, E>(wp, y);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        c[j] *= x[j];
+        s[j] *= interleaved ? y[j ^ 1] : y[j];
+      }
+    }
+  }
+  for (int h = 0;;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (h + i >= n) break;
+      if (h + i >= p.n) break;
       if constexpr (ROTATE) {
-        float x[E];
+        float x[E], y[E];
         unpack<T, E>(v[i], x);
-        if (w) {
+        if (interleaved) {
+#pragma unroll
+          for (int j = 0; j < E; ++j) y[j] = x[j ^ 1];
+        } else {
+          V o;
+#pragma unroll
+          for (int j = 0; j < (int)(E * sizeof(T) / 4); ++j) o.w[j] = __shfl_sync(mask, v[i].w[j], partner);
+          unpack<T, E>(o, y);
+        }
+        float inv = 1.f;
+        if (p.w) {
           float ss = 0.f;
 #pragma unroll
           for (int j = 0; j < E; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-          const float inv = rsqrtf(ss * (1.f / D) + eps);
-#pragma unroll
-          for (int j = 0; j < E; ++j) x[j] = x[j] * inv * wf[j];
+          inv = rsqrtf(ss * (1.f / D) + eps);
         }
-        if (interleaved) {
 #pragma unroll
-          for (int j = 0; j < E; j += 2) {
-            const float y = x[j], z = x[j + 1];
-            x[j] = y * c[j] + z * s[j];
-            x[j + 1] = z * c[j + 1] + y * s[j + 1];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const float z = __shfl_sync(mask, x[j], partner);
-            x[j] = x[j] * c[j] + z * s[j];
-          }
-        }
+        for (int j = 0; j < E; ++j) x[j] = (x[j] * c[j] + y[j] * s[j]) * inv;
         pack<T, E>(x, v[i]);
       }
-      v[i].store(dst + (h + i) * dst_step);
+      v[i].store(p.dst + (h + i) * p.dst_step + e0);
     }
+    h += kBatch;
+    if (h >= p.n) break;
+    load_heads<T, E>(v, p, h, e0);
   }
 }
 
 // One CTA: TOK neighbouring tokens of one (layer, sequence), 16 / TOK half-warps on each, and one of
-// `head_parts` equal shares of their heads.  E = d / 16 channels a lane.  A lane keeps the cosines and
-// sines of its channels for all heads of its token, and has kBatch heads' loads in flight.
-// (33,024 tokens of 28 + 4 + 4 heads, d = 128, bf16: from shared memory for each head 205 us.)
+// `head_parts` equal shares of their heads.  E = d / 16 channels a lane.  A lane keeps its cosines and
+// sines for all heads of its token and has kBatch heads' loads in flight, the first ones before the
+// angles are formed.  33,024 tokens of 28 + 4 + 4 heads, d = 128, bf16: 124 us, 4.9 TB/s of 6.46; eight
+// tokens a CTA took 205 us with cosines and sines read from shared memory for each head, 173 with a
+// shuffle for each normalised channel, 148 as it is.
 template <typename T, int E, int TOK>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a, int chunks, int head_parts) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) qk_norm_rope_kernel(const RopeArgs a, int chunks, int head_parts) {
   __shared__ float2 cs[TOK][8 * E];
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
@@ -161,83 +200,93 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   }
   if (r0 >= n) return;
   const int ntok = n - r0 < TOK ? n - r0 : TOK;
+
+  // this half-warp's token and share of the heads, in the order q, k, v
+  const int hw = threadIdx.x >> 4, t = min(hw / HS, ntok - 1);
+  const int e0 = (threadIdx.x & 15) * E;
+  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+  const int nq = a.q_in ? a.Hq : 0, nk = a.k_in ? a.Hkv : 0, nv = a.v_in ? a.Hkv : 0;
+  const int heads = nq + nk + nv, shares = HS * head_parts, share = part * HS + hw % HS;
+  const int h0 = (int)((int64_t)heads * share / shares);
+  const int h1 = hw / HS < ntok ? (int)((int64_t)heads * (share + 1) / shares) : h0;
+  auto part_of = [&](int which) {  // 0, 1, 2: q, k, v
+    const int64_t tok = (int64_t)lb * a.rows + r0 + t;
+    Part<T> p;
+    if (which == 0) {
+      p.src = static_cast<const T*>(a.q_in) + tok * a.q_stride + h0 * D;
+      p.dst = static_cast<T*>(a.q_out) + (((int64_t)lb * a.Hq + h0) * a.rows + r0 + t) * D;
+      p.dst_step = (int64_t)a.rows * D;
+      p.n = min(h1, nq) - h0;
+      p.w = static_cast<const T*>(a.q_w);
+    } else {
+      const int off = which == 1 ? nq : nq + nk, h = max(h0 - off, 0);
+      p.src = static_cast<const T*>(which == 1 ? a.k_in : a.v_in) + tok * (which == 1 ? a.k_stride : a.v_stride) + h * D;
+      p.dst = static_cast<T*>(which == 1 ? a.k_cache : a.v_cache) + (((int64_t)lb * a.Hkv + h) * a.cap + base + r0 + t) * D;
+      p.dst_step = a.cap * D;
+      p.n = min(h1 - off, which == 1 ? nk : nv) - h;
+      p.w = which == 1 ? static_cast<const T*>(a.k_w) : nullptr;
+    }
+    if (p.w) p.w += (int64_t)l * D;
+    return p;
+  };
+  // the first loads go out before the angles are formed
+  Vec<E * sizeof(T)> x[kBatch];
+  const int start = h0 < nq ? 0 : h0 < nq + nk ? 1 : 2;
+  if (h0 < h1) load_heads<T, E>(x, part_of(start), 0, e0);
+
   const int half = a.rot_dim >> 1;
   for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-    const int t = i / half, p = i - t * half;
+    const int tt = i / half, p = i - tt * half;
     const int axis = p < a.sec_end[0] ? 0 : p < a.sec_end[1] ? 1 : 2;
-    const double at = a.pos ? (double)a.pos[((int64_t)axis * a.B + b) * a.rows + r0 + t] : (double)(base + r0 + t);
+    const double at = a.pos ? (double)a.pos[((int64_t)axis * a.B + b) * a.rows + r0 + tt] : (double)(base + r0 + tt);
     double turns = at * a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
     sincospif(2.f * (float)turns, &s, &c);
-    cs[t][p] = make_float2(c, s);
+    cs[tt][p] = make_float2(c, s);
   }
   __syncthreads();
 
-  const int hw = threadIdx.x >> 4, t = hw / HS;
-  if (t >= ntok) return;
-  const int lane = threadIdx.x & 15, e0 = lane * E;
-  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
-  // Channel j of the lane becomes x_j c_j + x_partner s_j; past the rotated channels c = 1, s = 0.
-  // (E divides half, so a lane lies wholly in the first half, the second, or past both.)
-  float c[E], s[E];
-  int partner = threadIdx.x & 31;
-  if (a.interleaved) {
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int p = (e0 + j) >> 1;
-      const float2 f = p < half ? cs[t][p] : make_float2(1.f, 0.f);
-      c[j] = f.x;
-      s[j] = j & 1 ? f.y : -f.y;
-    }
-  } else {
-    const bool first = e0 < half, second = !first && e0 < a.rot_dim;
-    const int shift = half / E;
-    partner += first ? shift : second ? -shift : 0;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float2 f = first ? cs[t][e0 + j] : second ? cs[t][e0 - half + j] : make_float2(1.f, 0.f);
-      c[j] = f.x;
-      s[j] = first ? -f.y : f.y;
-    }
+  if (h0 >= h1) return;
+#pragma unroll 1
+  for (int which = start; which < 2; ++which) {
+    const Part<T> p = part_of(which);
+    if (p.n <= 0) continue;
+    if (which != start) load_heads<T, E>(x, p, 0, e0);
+    run_heads<T, E, true>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
   }
-
-  // this half-warp's share of the heads, in the order q, k, v
-  const int nq = a.q_in ? a.Hq : 0, nk = a.k_in ? a.Hkv : 0, nv = a.v_in ? a.Hkv : 0;
-  const int heads = nq + nk + nv, shares = HS * head_parts, share = part * HS + hw % HS;
-  const int h0 = (int)((int64_t)heads * share / shares), h1 = (int)((int64_t)heads * (share + 1) / shares);
-  const int64_t tok = (int64_t)lb * a.rows + r0 + t;
-  const int64_t row = base + r0 + t, q_step = (int64_t)a.rows * D, c_step = a.cap * D;
-  const int q1 = min(h1, nq), k0 = max(h0, nq), k1 = min(h1, nq + nk), v0 = max(h0, nq + nk);
-  if (h0 < q1)
-    run_heads<T, E, true>(static_cast<const T*>(a.q_in) + tok * a.q_stride + h0 * D + e0, D,
-                          static_cast<T*>(a.q_out) + ((int64_t)lb * a.Hq + h0) * q_step + (int64_t)(r0 + t) * D + e0,
-                          q_step, q1 - h0, a.q_w ? static_cast<const T*>(a.q_w) + (int64_t)l * D + e0 : nullptr, a.eps, c,
-                          s, partner, a.interleaved, mask);
-  if (k0 < k1)
-    run_heads<T, E, true>(static_cast<const T*>(a.k_in) + tok * a.k_stride + (k0 - nq) * D + e0, D,
-                          static_cast<T*>(a.k_cache) + ((int64_t)lb * a.Hkv + k0 - nq) * c_step + row * D + e0, c_step,
-                          k1 - k0, a.k_w ? static_cast<const T*>(a.k_w) + (int64_t)l * D + e0 : nullptr, a.eps, c, s,
-                          partner, a.interleaved, mask);
-  if (v0 < h1)  // (values are copied bit for bit)
-    run_heads<T, E, false>(static_cast<const T*>(a.v_in) + tok * a.v_stride + (v0 - nq - nk) * D + e0, D,
-                           static_cast<T*>(a.v_cache) + ((int64_t)lb * a.Hkv + v0 - nq - nk) * c_step + row * D + e0,
-                           c_step, h1 - v0, nullptr, 0.f, c, s, partner, false, mask);
+  const Part<T> p = part_of(2);
+  if (p.n > 0) {  // (values are copied bit for bit)
+    if (start != 2) load_heads<T, E>(x, p, 0, e0);
+    run_heads<T, E, false>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
+  }
 }
 
 template <typename T, int E>
 cudaError_t launch(const RopeArgs& a, int sms, cudaStream_t s) {
   const int heads = (a.q_in ? a.Hq : 0) + (a.k_in ? a.Hkv : 0) + (a.v_in ? a.Hkv : 0);
   const int64_t tokens = (int64_t)a.L * a.B * a.rows;
-  constexpr int TOK = 8;
-  if (tokens < 4 * (int64_t)sms) {  // few tokens: a CTA takes one token and up to kHeadsAtOnce of its heads
-    const int parts = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
+  // Tokens of a CTA: as few as fill the device about twice (once for few heads).  The fewer a CTA takes,
+  // the more half-warps share a token's heads and the sooner it is done; but each works out the token's
+  // coefficients for itself, which many CTAs feel.  28 + 4 + 4 heads, d = 128, bf16, us with 1 / 2 / 4 / 8 /
+  // 16 tokens a CTA: 8 tokens 3.3 / 4.7 / 7.3 / 9.9 / 11.7; 700 tokens 21.9 / 7.0 / 9.1 / 11.0 / 14.7; 2,800 tokens
+  // 83 / 25.5 / 22.6 / 18.8 / 21.2; 11,200 tokens 323 / 83 / 73 / 62 / 49.
+  const int64_t most = (int64_t)sms * (heads > kHeadsAtOnce ? 12 : 6) / 5;
+  auto go = [&](auto tok) {
+    constexpr int TOK = decltype(tok)::value;
+    const int chunks = (a.rows + TOK - 1) / TOK;
+    return launch_pdl(qk_norm_rope_kernel<T, E, TOK>, dim3((unsigned)((int64_t)a.L * a.B * chunks)), dim3(kThreads), 0, s,
+                      a, chunks, 1);
+  };
+  // one token: up to kHeadsAtOnce heads a CTA
+  const int parts = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
+  if (tokens * parts <= most)
     return launch_pdl(qk_norm_rope_kernel<T, E, 1>, dim3((unsigned)(tokens * parts)), dim3(kThreads), 0, s, a, a.rows,
                       parts);
-  }
-  const int chunks = (a.rows + TOK - 1) / TOK;
-  return launch_pdl(qk_norm_rope_kernel<T, E, TOK>, dim3((unsigned)((int64_t)a.L * a.B * chunks)), dim3(kThreads), 0, s,
-                    a, chunks, 1);
+  if (tokens <= 2 * most) return go(std::integral_constant<int, 2>());
+  if (tokens <= 4 * most) return go(std::integral_constant<int, 4>());
+  if (tokens <= 8 * most) return go(std::integral_constant<int, 8>());
+  return go(std::integral_constant<int, 16>());
 }
 
 }  // namespace
