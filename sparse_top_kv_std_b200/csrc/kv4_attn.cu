@@ -135,7 +135,8 @@ __device__ __forceinline__ Unit locate(const Kv4AttnArgs& a, const int* cum, int
   return u;
 }
 
-__device__ __forceinline__ int cta_begin(int tiles, int ctas, int c) { return (int)((int64_t)tiles * c / ctas); }
+// Tiles of a CTA: CTA c has tiles [c share, (c + 1) share).
+__device__ __forceinline__ int cta_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
 
 // ---------------------------------------------------------------- instructions
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -744,7 +745,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   __syncthreads();
   const int total = ctl.cum[a.B] * a.Hkv * a.row_blocks * a.L;
   if (total == 0) return;
-  const int begin = cta_begin(total, gridDim.x, blockIdx.x), end = cta_begin(total, gridDim.x, blockIdx.x + 1);
+  const int share = cta_share(total, gridDim.x);
+  const int64_t begin64 = (int64_t)share * blockIdx.x;
+  const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
   const uint32_t ring = smem_u32(smem);
   if (tid == 0) {
     ctl.next = begin;
@@ -826,33 +829,29 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int
   __shared__ float lsum[LANES];
   __shared__ float topw[8];
   const int tid = threadIdx.x;
-  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
-  pdl_trigger();
+  // The attention kernel lets this one start once it has itself waited for the kernels before it, so the
+  // lengths can be read, and the slots found, while it runs.
   if (tid < 32) scan_tiles(a, cum, tid, false);
   __syncthreads();
   const int per = cum[a.B] * a.Hkv * a.row_blocks;
-  const int total = per * a.L;
   int id = blockIdx.x;  // ((l * B + b) * Hkv + h) * rows + r
   const int r = id % a.rows;
   id /= a.rows;
   const int h = id % a.Hkv, lb = id / a.Hkv, b = lb % a.B, l = lb / a.B;
   const int tiles = cum[b + 1] - cum[b];
-  if (tiles == 0) return;
   const int rb = r / ROWS, n = r - rb * ROWS;
   const int u0 = l * per + cum[b] * a.Hkv * a.row_blocks + (h * a.row_blocks + rb) * tiles;
-  // the CTA that holds tile x is the last c with floor(total c / ctas) <= x
-  const int c0 = (int)((((int64_t)u0 + 1) * ctas - 1) / total);
-  const int c1 = (int)((((int64_t)u0 + tiles) * ctas - 1) / total);
-  if (c0 == c1) return;  // written whole
+  const int share = cta_share(per * a.L, ctas);
+  const int c0 = tiles ? u0 / share : 0, c1 = tiles ? (u0 + tiles - 1) / share : 0;
+  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
+  pdl_trigger();
+  if (c0 == c1) return;  // written whole, or not valid
   const int lane = tid % LPR, first = tid / LPR;
-  auto slot_of = [&](int c) -> const float* {
-    const int s = cta_begin(total, ctas, c);
-    if (s == cta_begin(total, ctas, c + 1)) return nullptr;
-    return a.ws + (2 * (int64_t)c + (u0 <= s ? 0 : 1)) * slot_floats<D>(ROWS);
+  auto slot_of = [&](int c) -> const float* {  // (the first CTA's slot 1 unless its range begins with the unit)
+    return a.ws + (2 * (int64_t)c + (c > c0 || c * share == u0 ? 0 : 1)) * slot_floats<D>(ROWS);
   };
   float top = -INFINITY;
-  for (int c = c0 + tid; c <= c1; c += 256)
-    if (const float* p = slot_of(c)) top = fmaxf(top, p[ROWS * D + 2 * n]);
+  for (int c = c0 + tid; c <= c1; c += 256) top = fmaxf(top, slot_of(c)[ROWS * D + 2 * n]);
   top = warp_max(top);
   if ((tid & 31) == 0) topw[tid >> 5] = top;
   __syncthreads();
@@ -860,9 +859,9 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int
   for (int w = 0; w < 8; ++w) top = fmaxf(top, topw[w]);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   float lt = 0.f;
+#pragma unroll 4
   for (int c = c0 + first; c <= c1; c += LANES) {
     const float* p = slot_of(c);
-    if (!p) continue;
     const float2 ml = *reinterpret_cast<const float2*>(p + ROWS * D + 2 * n);
     const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
     const float4 v = *reinterpret_cast<const float4*>(p + n * D + 4 * lane);
