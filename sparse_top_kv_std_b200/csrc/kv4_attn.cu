@@ -818,17 +818,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
 
 // Units that several CTAs touched: one CTA for each query row merges their slots.
 //   M = max_c m_c,  o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
+// D / 4 lanes hold a slot's row, blockDim.y slots are read at a time (so that a row's slots come in one or
+// two trips to memory), and each lane merges its slots as it goes.
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int ctas) {
+__global__ void __launch_bounds__(1024) kv4_merge_kernel(const Kv4AttnArgs a, int ctas) {
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-  constexpr int ROWS = 8 * NT;
-  constexpr int LPR = D / 4;             // lanes of a row, four channels each
-  constexpr int LANES = 256 / LPR;       // slots read at a time
+  constexpr int ROWS = 8 * NT, LPR = D / 4;
   __shared__ int cum[kKv4AttnMaxB + 1];
-  __shared__ float4 part[LANES][LPR];
-  __shared__ float lsum[LANES];
-  __shared__ float topw[8];
-  const int tid = threadIdx.x;
+  __shared__ float4 part[1024 / LPR][LPR];
+  __shared__ float2 stat[1024 / LPR];
+  const int lane = threadIdx.x, first = threadIdx.y, tid = first * LPR + lane;
   // The attention kernel lets this one start once it has itself waited for the kernels before it, so the
   // lengths can be read, and the slots found, while it runs.
   if (tid < 32) scan_tiles(a, cum, tid, false);
@@ -846,44 +845,55 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnArgs a, int
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
   if (c0 == c1) return;  // written whole, or not valid
-  const int lane = tid % LPR, first = tid / LPR;
-  auto slot_of = [&](int c) -> const float* {  // (the first CTA's slot 1 unless its range begins with the unit)
-    return a.ws + (2 * (int64_t)c + (c > c0 || c * share == u0 ? 0 : 1)) * slot_floats<D>(ROWS);
-  };
-  float top = -INFINITY;
-  for (int c = c0 + tid; c <= c1; c += 256) top = fmaxf(top, slot_of(c)[ROWS * D + 2 * n]);
-  top = warp_max(top);
-  if ((tid & 31) == 0) topw[tid >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, topw[w]);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lt = 0.f;
-#pragma unroll 4
-  for (int c = c0 + first; c <= c1; c += LANES) {
-    const float* p = slot_of(c);
-    const float2 ml = *reinterpret_cast<const float2*>(p + ROWS * D + 2 * n);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    const float4 v = *reinterpret_cast<const float4*>(p + n * D + 4 * lane);
-    sum.x = fmaf(f, v.x, sum.x); sum.y = fmaf(f, v.y, sum.y);
-    sum.z = fmaf(f, v.z, sum.z); sum.w = fmaf(f, v.w, sum.w);
-    lt = fmaf(f, ml.y, lt);
+  float top = -INFINITY, lt = 0.f;
+  for (int c = c0 + first; c <= c1; c += 4 * blockDim.y) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ci = c + i * (int)blockDim.y;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ci <= c1) {  // (the first CTA's slot 1, unless its range begins with the unit)
+        const float* p = a.ws + (2 * (int64_t)ci + (ci > c0 || ci * share == u0 ? 0 : 1)) * slot_floats<D>(ROWS);
+        ml[i] = *reinterpret_cast<const float2*>(p + ROWS * D + 2 * n);
+        v[i] = *reinterpret_cast<const float4*>(p + n * D + 4 * lane);
+      }
+    }
+    const float m1 = fmaxf(top, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+    const float keep = top == -INFINITY ? 0.f : ex2(top - m1);
+    sum.x *= keep; sum.y *= keep; sum.z *= keep; sum.w *= keep;
+    lt *= keep;
+    top = m1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - top);
+      sum.x = fmaf(f, v[i].x, sum.x); sum.y = fmaf(f, v[i].y, sum.y);
+      sum.z = fmaf(f, v[i].z, sum.z); sum.w = fmaf(f, v[i].w, sum.w);
+      lt = fmaf(f, ml[i].y, lt);
+    }
   }
   part[first][lane] = sum;
-  if (lane == 0) lsum[first] = lt;
+  if (lane == 0) stat[first] = make_float2(top, lt);
   __syncthreads();
-  if (tid < LPR) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < LANES; ++i) {
-      const float4 v = part[i][tid];
-      o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-      s += lsum[i];
+  if (first == 0) {
+    top = -INFINITY;
+    for (int i = 0; i < (int)blockDim.y; ++i) top = fmaxf(top, stat[i].x);
+    sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    lt = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < (int)blockDim.y; ++i) {
+      const float2 ml = stat[i];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      const float4 v = part[i][lane];
+      sum.x = fmaf(f, v.x, sum.x); sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z); sum.w = fmaf(f, v.w, sum.w);
+      lt = fmaf(f, ml.y, lt);
     }
-    const float inv = s == 0.f ? 0.f : 1.f / s;
-    const int64_t at = (((int64_t)lb * a.Hq + h * a.G) * a.nq + r) * D + 4 * tid;
-    store4(static_cast<T*>(a.o) + at, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    const int64_t at = (((int64_t)lb * a.Hq + h * a.G) * a.nq + r) * D + 4 * lane;
+    store4(static_cast<T*>(a.o) + at, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
   }
 }
 
@@ -903,7 +913,11 @@ cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
   e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), Lay::BYTES, s, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.L * a.B * a.Hkv * a.rows;
-  return launch_pdl(kv4_merge_kernel<D, NT, F32>, dim3((unsigned)rows), dim3(256), 0, s, a, a.ctas);
+  // slots of a unit if all are equally long: four for each lane of the merge
+  const int slots = a.ctas / (a.L * a.B * a.Hkv * a.row_blocks) + 2;
+  int at_once = 128 / (D / 4);
+  while (at_once < 1024 / (D / 4) && 4 * at_once < slots) at_once *= 2;
+  return launch_pdl(kv4_merge_kernel<D, NT, F32>, dim3((unsigned)rows), dim3(D / 4, at_once), 0, s, a, a.ctas);
 }
 
 }  // namespace
