@@ -65,6 +65,104 @@ struct Layout {
   static constexpr int BYTES = AT_MERGE + MERGE;
 };
 
+// ---------------------------------------------------------------- work split
+// Units are numbered (layer, sequence, KV head, row block).  A unit's tiles are cut into groups of
+// `group`, all units' groups form one sequence, and CTA c takes groups [c share, (c + 1) share) of it.
+// Long work is cut tile by tile (group = 1): every CTA has the same number of tiles to within one, and
+// those that straddle two units pay for it with a second set of queries and a second merge, some 2.5
+// us.  Where that is more than the tiles it saves, units are cut into equal parts, one a CTA
+// (share = 1).
+struct Split {
+  int cum[kKv4AttnMaxB + 1];  // groups of the sequences before b, in one (layer, head, row block)
+  int group, share, total;
+};
+
+struct Unit {
+  int l, b, h, rb;
+  int first, groups;  // the group within the unit; the unit's groups
+};
+
+// Keys that sequence b's last query position attends; -1: not valid.  (Read again from the length
+// wherever it is needed: after the first time that is a hit in L1.)
+__device__ __forceinline__ int keys_of(const Kv4AttnArgs& a, int b) {
+  const int len = a.len[b];
+  const int64_t n = (int64_t)len + a.len_off + a.nq - 1;
+  return len >= 0 && n <= a.cap ? (int)n : -1;
+}
+__device__ __forceinline__ int tiles_of(int keys) { return keys < 0 ? 0 : keys < 1 ? 1 : (keys + kTile - 1) / kTile; }
+
+// The split of this call's work over `ctas` CTAs, by one warp.  (The first 32 sequences stay in
+// registers: a draft step of a few sequences waits for this.)
+__device__ __forceinline__ void plan_split(const Kv4AttnArgs& a, Split* sp, int ctas, int lane, bool flag) {
+  const int units = a.Hkv * a.row_blocks * a.L;  // of one sequence
+  auto load = [&](int b) {
+    if (b >= a.B) return 0;
+    const int keys = keys_of(a, b);
+    if (keys < 0 && flag) flag_error(a.err, STD_DEVERR_LENGTH);
+    return tiles_of(keys);
+  };
+  const int mine = load(lane);
+  int sum = mine;
+  for (int b = lane + 32; b < a.B; b += 32) sum += load(b);
+  flag = false;
+  sum = (a.B == 1 ? __shfl_sync(0xffffffffu, sum, 0) : __reduce_add_sync(0xffffffffu, sum)) * units;
+  int share = sum <= ctas ? (sum > 0) : (sum + ctas - 1) / ctas, group = 1;
+  if (share > 1 && share <= 32) {
+#pragma unroll 1
+    for (int s = share; s <= share + 2; ++s) {  // parts of s tiles
+      int parts = (mine + s - 1) / s;
+      for (int b = lane + 32; b < a.B; b += 32) parts += (load(b) + s - 1) / s;
+      parts = __reduce_add_sync(0xffffffffu, parts) * units;
+      if (parts <= ctas) {
+        group = s;
+        share = 1;
+        sum = parts;
+        break;
+      }
+    }
+  }
+  if (lane == 0) {
+    sp->cum[0] = 0;
+    sp->group = group;
+    sp->share = share;
+    sp->total = sum;
+  }
+  int run = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int s = b0 == 0 ? mine : load(b);
+    if (group > 1) s = (s + group - 1) / group;
+    for (int o = 1; o < 32 && o < a.B; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (b < a.B) sp->cum[b + 1] = run + s;
+    run += __shfl_sync(0xffffffffu, s, 31);
+  }
+}
+
+// The unit that group x of the sequence belongs to.
+__device__ __forceinline__ Unit locate(const Kv4AttnArgs& a, const Split& sp, int x) {
+  Unit u;
+  const int heads = a.Hkv * a.row_blocks;
+  const int layer = sp.cum[a.B] * heads;  // groups of a layer
+  u.l = a.L == 1 ? 0 : x / layer;
+  int r = x - u.l * layer;
+  int lo = 0, hi = a.B;  // the last b with cum[b] * heads <= r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sp.cum[mid] * heads <= r) lo = mid; else hi = mid;
+  }
+  u.b = lo;
+  r -= sp.cum[lo] * heads;
+  u.groups = sp.cum[lo + 1] - sp.cum[lo];
+  const int hr = r / u.groups;
+  u.first = r - hr * u.groups;
+  u.h = a.row_blocks == 1 ? hr : hr / a.row_blocks;
+  u.rb = hr - u.h * a.row_blocks;
+  return u;
+}
+
 constexpr int kMaxStages = 16;
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -72,71 +170,9 @@ struct Ctl {
   int fills, next, left, first, keys;
   int64_t row0;  // cache row of the unit's row 0
   float m[kWarps][16], l[kWarps][16];
-  int cum[kKv4AttnMaxB + 1];  // tiles of the sequences before b
+  Split split;
   volatile int abort;
 };
-
-// ---------------------------------------------------------------- work split
-// Units are numbered (layer, sequence, KV head, row block); sequence b has tiles(b) tiles in each.
-struct Unit {
-  int l, b, h, rb, tile0, tiles;  // tile0: the tile within the unit; tiles: the unit's
-};
-
-__device__ __forceinline__ int seq_tiles(const Kv4AttnArgs& a, int b, int* keys) {
-  const int64_t n0 = (int64_t)a.len[b] + a.len_off, n = n0 + a.nq - 1;
-  if (a.len[b] < 0 || n > a.cap) return -1;
-  *keys = (int)n;
-  return n < 1 ? 1 : (int)((n + kTile - 1) / kTile);
-}
-
-// Prefix sums of the sequences' tiles by one warp; an invalid sequence has none.
-__device__ __forceinline__ void scan_tiles(const Kv4AttnArgs& a, int* cum, int lane, bool flag) {
-  int run = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int keys, t = 0;
-    if (b < a.B) {
-      t = seq_tiles(a, b, &keys);
-      if (t < 0) {
-        if (flag) flag_error(a.err, STD_DEVERR_LENGTH);
-        t = 0;
-      }
-    }
-    int s = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (b < a.B) cum[b + 1] = run + s;
-    run += __shfl_sync(0xffffffffu, s, 31);
-  }
-  if (lane == 0) cum[0] = 0;
-}
-
-__device__ __forceinline__ Unit locate(const Kv4AttnArgs& a, const int* cum, int t) {
-  Unit u;
-  const int per_tile = a.Hkv * a.row_blocks;
-  const int tl = cum[a.B] * per_tile;  // tiles of a layer
-  u.l = t / tl;
-  int r = t - u.l * tl;
-  int lo = 0, hi = a.B;  // the last b with cum[b] * per_tile <= r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] * per_tile <= r) lo = mid; else hi = mid;
-  }
-  u.b = lo;
-  r -= cum[lo] * per_tile;
-  u.tiles = cum[lo + 1] - cum[lo];
-  const int hr = r / u.tiles;
-  u.tile0 = r - hr * u.tiles;
-  u.h = hr / a.row_blocks;
-  u.rb = hr - u.h * a.row_blocks;
-  return u;
-}
-
-// Tiles of a CTA: CTA c has tiles [c share, (c + 1) share).
-__device__ __forceinline__ int cta_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
 
 // ---------------------------------------------------------------- instructions
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -636,29 +672,19 @@ __device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4Attn
           st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], 1048576.f, c);  // 2^20
         }
       }
-      if (g == 0) {
-        ctl->m[warp][nt * 8 + 2 * t + e] = st.M[nt][e];
-        ctl->l[warp][nt * 8 + 2 * t + e] = st.l[nt][e];
-      }
-    }
-  __syncthreads();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
       const int n = nt * 8 + 2 * t + e;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ctl->m[w][n]);
-      const float f = st.M[nt][e] == -INFINITY ? 0.f : ex2(st.M[nt][e] - top);
+      if (g == 0) {
+        ctl->m[warp][n] = st.M[nt][e];
+        ctl->l[warp][n] = st.l[nt][e];
+      }
       float* row = buf + (warp * Lay::ROWS + n) * Lay::OSTR;
 #pragma unroll
       for (int gr = 0; gr < S::GR; ++gr)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           *reinterpret_cast<float4*>(row + gr * 64 + 8 * g + 4 * i) =
-              make_float4(st.o[nt][gr * 4 + 2 * i][e] * f, st.o[nt][gr * 4 + 2 * i][2 + e] * f,
-                          st.o[nt][gr * 4 + 2 * i + 1][e] * f, st.o[nt][gr * 4 + 2 * i + 1][2 + e] * f);
+              make_float4(st.o[nt][gr * 4 + 2 * i][e], st.o[nt][gr * 4 + 2 * i][2 + e], st.o[nt][gr * 4 + 2 * i + 1][e],
+                          st.o[nt][gr * 4 + 2 * i + 1][2 + e]);
     }
   __syncthreads();
   for (int i = warp * 32 + lane; i < Lay::ROWS * (D / 4); i += kWarps * 32) {
@@ -672,9 +698,11 @@ __device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4Attn
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float m = ctl->m[w][n];
-      l += m == -INFINITY ? 0.f : ctl->l[w][n] * ex2(m - top);
+      const float f = m == -INFINITY ? 0.f : ex2(m - top);
+      l = fmaf(f, ctl->l[w][n], l);
       const float4 v = *reinterpret_cast<const float4*>(buf + (w * Lay::ROWS + n) * Lay::OSTR + c);
-      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+      sum.x = fmaf(f, v.x, sum.x); sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z); sum.w = fmaf(f, v.w, sum.w);
     }
     if (whole) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that attends no key: zeros
@@ -694,15 +722,14 @@ template <int D, int NT, bool F32>
 __device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Ctl* ctl, uint32_t ring, int end) {
   using Lay = Layout<D, NT, F32>;
   while (ctl->left == 0) {
-    const int t = ctl->next;
-    if (t >= end) return;
-    const Unit u = locate(a, ctl->cum, t);
-    const int n = min(u.tiles - u.tile0, end - t);
-    int keys = 0;
-    seq_tiles(a, u.b, &keys);
-    ctl->next = t + n;
-    ctl->left = keys > u.tile0 * kTile ? n : 0;  // (a sequence without keys has nothing to fetch)
-    ctl->first = u.tile0 * kTile;
+    const int x = ctl->next;
+    if (x >= end) return;
+    const Unit u = locate(a, ctl->split, x);
+    const int n = min(u.groups - u.first, end - x), group = ctl->split.group;
+    const int keys = keys_of(a, u.b), first = u.first * group;
+    ctl->next = x + n;
+    ctl->left = min(n * group, (keys + kTile - 1) / kTile - first);  // (none for a sequence without keys)
+    ctl->first = first * kTile;
     ctl->keys = keys;
     ctl->row0 = (((int64_t)u.l * a.B + u.b) * a.Hkv + u.h) * a.cap;
   }
@@ -741,13 +768,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   }
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
-  if (warp == 0) scan_tiles(a, ctl.cum, lane, blockIdx.x == 0);
+  if (warp == 0) plan_split(a, &ctl.split, gridDim.x, lane, blockIdx.x == 0);
   __syncthreads();
-  const int total = ctl.cum[a.B] * a.Hkv * a.row_blocks * a.L;
-  if (total == 0) return;
-  const int share = cta_share(total, gridDim.x);
+  const int total = ctl.split.total, share = ctl.split.share;
   const int64_t begin64 = (int64_t)share * blockIdx.x;
-  const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
+  if (begin64 >= total) return;
+  const int begin = (int)begin64, end = min(begin + share, total);
   const uint32_t ring = smem_u32(smem);
   if (tid == 0) {
     ctl.next = begin;
@@ -760,11 +786,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     State<D, NT, F32> st;
     int key0, n0, left, rb;
     {
-      const Unit u = locate(a, ctl.cum, t);
-      int keys = 0;
-      seq_tiles(a, u.b, &keys);
-      key0 = u.tile0 * kTile;
-      left = min(min(u.tiles - u.tile0, end - t), (keys - key0 + kTile - 1) / kTile);  // (no keys: no tile to read)
+      const Unit u = locate(a, ctl.split, t);
+      const int keys = keys_of(a, u.b), group = ctl.split.group, first = u.first * group;
+      key0 = first * kTile;
+      left = min(min(u.groups - u.first, end - t) * group, (keys + kTile - 1) / kTile - first);  // (may be none)
       n0 = keys - a.nq + 1;  // keys that query position 0 attends
       rb = u.rb;
       load_queries<D, NT, F32>(st, a, u, ring + Lay::AT_Q, warp == 0, lane);
@@ -799,9 +824,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
         phase ^= 1;
       }
     }
-    const Unit u = locate(a, ctl.cum, t);
-    const int n = min(u.tiles - u.tile0, end - t);
-    const bool whole = n == u.tiles;
+    const Unit u = locate(a, ctl.split, t);
+    const int n = min(u.groups - u.first, end - t);
+    const bool whole = n == u.groups;
     float* slot = nullptr;
     if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(Lay::ROWS);
     if (!finish_unit<D, NT, F32>(st, a, u, &ctl, reinterpret_cast<float*>(smem + Lay::AT_MERGE), whole, slot, warp,
@@ -824,24 +849,22 @@ template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(1024) kv4_merge_kernel(const Kv4AttnArgs a, int ctas) {
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int ROWS = 8 * NT, LPR = D / 4;
-  __shared__ int cum[kKv4AttnMaxB + 1];
+  __shared__ Split sp;
   __shared__ float4 part[1024 / LPR][LPR];
   __shared__ float2 stat[1024 / LPR];
   const int lane = threadIdx.x, first = threadIdx.y, tid = first * LPR + lane;
   // The attention kernel lets this one start once it has itself waited for the kernels before it, so the
   // lengths can be read, and the slots found, while it runs.
-  if (tid < 32) scan_tiles(a, cum, tid, false);
+  if (tid < 32) plan_split(a, &sp, ctas, tid, false);
   __syncthreads();
-  const int per = cum[a.B] * a.Hkv * a.row_blocks;
   int id = blockIdx.x;  // ((l * B + b) * Hkv + h) * rows + r
   const int r = id % a.rows;
   id /= a.rows;
   const int h = id % a.Hkv, lb = id / a.Hkv, b = lb % a.B, l = lb / a.B;
-  const int tiles = cum[b + 1] - cum[b];
+  const int heads = a.Hkv * a.row_blocks, groups = sp.cum[b + 1] - sp.cum[b], share = sp.share;
   const int rb = r / ROWS, n = r - rb * ROWS;
-  const int u0 = l * per + cum[b] * a.Hkv * a.row_blocks + (h * a.row_blocks + rb) * tiles;
-  const int share = cta_share(per * a.L, ctas);
-  const int c0 = tiles ? u0 / share : 0, c1 = tiles ? (u0 + tiles - 1) / share : 0;
+  const int u0 = (l * sp.cum[a.B] + sp.cum[b]) * heads + (h * a.row_blocks + rb) * groups;
+  const int c0 = groups ? u0 / share : 0, c1 = groups ? (u0 + groups - 1) / share : 0;
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
   if (c0 == c1) return;  // written whole, or not valid
