@@ -277,6 +277,9 @@ struct Kv4AttnArgs {
 };
 void plan_kv4_attn(Kv4AttnArgs* a, int sms);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
+// Its kernel for many query rows (kv4_attn_tc.cu), in blocks of kv4_attn_tc_rows().
+int kv4_attn_tc_rows();
+cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, cudaStream_t s);
 
 cudaError_t launch_accept(int B, int gamma, const int32_t* draft, const int32_t* dense,
                           int32_t* n_plus_1, int32_t* accepted, cudaStream_t s);

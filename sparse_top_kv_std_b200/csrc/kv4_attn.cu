@@ -26,10 +26,7 @@
 // the CTAs split evenly; bulk copies stream the tiles through a shared-memory ring, and each of
 // eight warps takes 16 keys of every tile with a softmax state of its own.  The states merge once for each unit a CTA touches; units that several CTAs touch merge
 // in a second kernel.
-#include "common.cuh"
-#include "internal.h"
-#include "kv4.cuh"
-#include "tc100.cuh"
+#include "kv4_attn.cuh"
 
 #include <cuda_fp16.h>
 
@@ -39,7 +36,6 @@
 namespace stdb {
 namespace {
 
-constexpr int kTile = 128;               // keys of a tile
 constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLimit = 32768.f;        // largest weight x scale that goes to fp16
@@ -65,121 +61,16 @@ struct Layout {
   static constexpr int BYTES = AT_MERGE + MERGE;
 };
 
-// ---------------------------------------------------------------- work split
-// Units are numbered (layer, sequence, KV head, row block).  A unit's tiles are cut into groups of
-// `group`, all units' groups form one sequence, and CTA c takes groups [c share, (c + 1) share) of it.
-// Long work is cut tile by tile (group = 1): every CTA has the same number of tiles to within one, and
-// those that straddle two units pay for it with a second set of queries and a second merge, some 2.5
-// us.  Where that is more than the tiles it saves, units are cut into equal parts, one a CTA
-// (share = 1).
-struct Split {
-  int cum[kKv4AttnMaxB + 1];  // groups of the sequences before b, in one (layer, head, row block)
-  int group, share, total;
-};
-
-struct Unit {
-  int l, b, h, rb;
-  int first, groups;  // the group within the unit; the unit's groups
-};
-
-// Keys that sequence b's last query position attends; -1: not valid.  (Read again from the length
-// wherever it is needed: after the first time that is a hit in L1.)
-__device__ __forceinline__ int keys_of(const Kv4AttnArgs& a, int b) {
-  const int len = a.len[b];
-  const int64_t n = (int64_t)len + a.len_off + a.nq - 1;
-  return len >= 0 && n <= a.cap ? (int)n : -1;
-}
-__device__ __forceinline__ int tiles_of(int keys) { return keys < 0 ? 0 : keys < 1 ? 1 : (keys + kTile - 1) / kTile; }
-
-// The split of this call's work over `ctas` CTAs, by one warp.  (The first 32 sequences stay in
-// registers: a draft step of a few sequences waits for this.)
-__device__ __forceinline__ void plan_split(const Kv4AttnArgs& a, Split* sp, int ctas, int lane, bool flag) {
-  const int units = a.Hkv * a.row_blocks * a.L;  // of one sequence
-  auto load = [&](int b) {
-    if (b >= a.B) return 0;
-    const int keys = keys_of(a, b);
-    if (keys < 0 && flag) flag_error(a.err, STD_DEVERR_LENGTH);
-    return tiles_of(keys);
-  };
-  const int mine = load(lane);
-  int sum = mine;
-  for (int b = lane + 32; b < a.B; b += 32) sum += load(b);
-  flag = false;
-  sum = (a.B == 1 ? __shfl_sync(0xffffffffu, sum, 0) : __reduce_add_sync(0xffffffffu, sum)) * units;
-  int share = sum <= ctas ? (sum > 0) : (sum + ctas - 1) / ctas, group = 1;
-  if (share > 1 && share <= 32) {
-#pragma unroll 1
-    for (int s = share; s <= share + 2; ++s) {  // parts of s tiles
-      int parts = (mine + s - 1) / s;
-      for (int b = lane + 32; b < a.B; b += 32) parts += (load(b) + s - 1) / s;
-      parts = __reduce_add_sync(0xffffffffu, parts) * units;
-      if (parts <= ctas) {
-        group = s;
-        share = 1;
-        sum = parts;
-        break;
-      }
-    }
-  }
-  if (lane == 0) {
-    sp->cum[0] = 0;
-    sp->group = group;
-    sp->share = share;
-    sp->total = sum;
-  }
-  int run = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int s = b0 == 0 ? mine : load(b);
-    if (group > 1) s = (s + group - 1) / group;
-    for (int o = 1; o < 32 && o < a.B; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (b < a.B) sp->cum[b + 1] = run + s;
-    run += __shfl_sync(0xffffffffu, s, 31);
-  }
-}
-
-// The unit that group x of the sequence belongs to.
-__device__ __forceinline__ Unit locate(const Kv4AttnArgs& a, const Split& sp, int x) {
-  Unit u;
-  const int heads = a.Hkv * a.row_blocks;
-  const int layer = sp.cum[a.B] * heads;  // groups of a layer
-  u.l = a.L == 1 ? 0 : x / layer;
-  int r = x - u.l * layer;
-  int lo = 0, hi = a.B;  // the last b with cum[b] * heads <= r
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sp.cum[mid] * heads <= r) lo = mid; else hi = mid;
-  }
-  u.b = lo;
-  r -= sp.cum[lo] * heads;
-  u.groups = sp.cum[lo + 1] - sp.cum[lo];
-  const int hr = r / u.groups;
-  u.first = r - hr * u.groups;
-  u.h = a.row_blocks == 1 ? hr : hr / a.row_blocks;
-  u.rb = hr - u.h * a.row_blocks;
-  return u;
-}
-
 constexpr int kMaxStages = 16;
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  // the next tile to fetch (touched only by the thread that fetches it)
-  int fills, next, left, first, keys;
-  int64_t row0;  // cache row of the unit's row 0
+  Fetch fetch;
   float m[kWarps][16], l[kWarps][16];
   Split split;
   volatile int abort;
 };
 
 // ---------------------------------------------------------------- instructions
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -219,8 +110,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
@@ -633,19 +522,6 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = v;
-  } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  }
-}
-
-// Partials of one slot: [8 NT][D] unnormalised sums, then [8 NT][2] (reference, sum of weights).
-template <int D>
-__host__ __device__ constexpr int64_t slot_floats(int rows) { return (int64_t)rows * (D + 2); }
-
 // Merge the warps' states of one unit and write the output (`whole`) or the partial slot.  False,
 // to every thread, once a wait has given up: nothing is written then.
 template <int D, int NT, bool F32>
@@ -717,38 +593,6 @@ __device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4Attn
   return true;
 }
 
-// Fetch the next tile of this CTA's range into its stage (one thread at a time, in order).
-template <int D, int NT, bool F32>
-__device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Ctl* ctl, uint32_t ring, int end) {
-  using Lay = Layout<D, NT, F32>;
-  while (ctl->left == 0) {
-    const int x = ctl->next;
-    if (x >= end) return;
-    const Unit u = locate(a, ctl->split, x);
-    const int n = min(u.groups - u.first, end - x), group = ctl->split.group;
-    const int keys = keys_of(a, u.b), first = u.first * group;
-    ctl->next = x + n;
-    ctl->left = min(n * group, (keys + kTile - 1) / kTile - first);  // (none for a sequence without keys)
-    ctl->first = first * kTile;
-    ctl->keys = keys;
-    ctl->row0 = (((int64_t)u.l * a.B + u.b) * a.Hkv + u.h) * a.cap;
-  }
-  const int first = ctl->first, stage = ctl->fills % Lay::STAGES;
-  // whole 16-row blocks: the capacity is a multiple of 16, so they end inside the cache
-  const uint32_t rows = min(kTile, (ctl->keys - first + 15) & ~15);
-  const int64_t row = ctl->row0 + first;
-  const uint32_t dst = ring + stage * Lay::STAGE;
-  uint64_t* bar = &ctl->full[stage];
-  tc::mbar_expect_tx(bar, 2 * rows * (Lay::CW + Lay::SW));
-  bulk_load(dst, a.k_codes + row * Lay::CW, rows * Lay::CW, bar);
-  bulk_load(dst + 2 * kTile * Lay::CW, a.k_scales + row * Lay::SW, rows * Lay::SW, bar);
-  bulk_load(dst + kTile * Lay::CW, a.v_codes + row * Lay::CW, rows * Lay::CW, bar);
-  bulk_load(dst + kTile * (2 * Lay::CW + Lay::SW), a.v_scales + row * Lay::SW, rows * Lay::SW, bar);
-  ctl->fills += 1;
-  ctl->first = first + kTile;
-  ctl->left -= 1;
-}
-
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
   using Lay = Layout<D, NT, F32>;
@@ -763,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
       tc::mbar_init(&ctl.empty[s], kWarps);
     }
     ctl.abort = 0;
-    ctl.fills = ctl.left = 0;
+    ctl.fetch.fills = ctl.fetch.left = 0;
     tc::fence_mbar_init();
   }
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
@@ -776,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   const int begin = (int)begin64, end = min(begin + share, total);
   const uint32_t ring = smem_u32(smem);
   if (tid == 0) {
-    ctl.next = begin;
-    for (int s = 0; s < STAGES; ++s) fetch_tile<D, NT, F32>(a, &ctl, ring, end);
+    ctl.fetch.next = begin;
+    for (int s = 0; s < STAGES; ++s) fetch_tile<D, STAGES>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
   }
   const LaneAt<D, NT, F32> at(warp, lane);
   int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
@@ -812,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
         if (turn == warp) {
           const int before = stage == 0 ? STAGES - 1 : stage - 1;
           if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
-            fetch_tile<D, NT, F32>(a, &ctl, ring, end);
+            fetch_tile<D, STAGES>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
         }
         tc::mbar_arrive(&ctl.empty[stage]);
       }
@@ -836,87 +680,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
   }
   if (ctl.abort && tid == 0) {  // the copies in flight land in this CTA's shared memory: wait for them
     volatile int none = 0;
-    for (int k = max(0, ctl.fills - STAGES); k < ctl.fills; ++k)
+    for (int k = max(0, ctl.fetch.fills - STAGES); k < ctl.fetch.fills; ++k)
       tc::mbar_wait(&ctl.full[k % STAGES], (uint32_t)(k / STAGES) & 1u, &none, a.err);
-  }
-}
-
-// Units that several CTAs touched: one CTA for each query row merges their slots.
-//   M = max_c m_c,  o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
-// D / 4 lanes hold a slot's row, blockDim.y slots are read at a time (so that a row's slots come in one or
-// two trips to memory), and each lane merges its slots as it goes.
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(1024) kv4_merge_kernel(const Kv4AttnArgs a, int ctas) {
-  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-  constexpr int ROWS = 8 * NT, LPR = D / 4;
-  __shared__ Split sp;
-  __shared__ float4 part[1024 / LPR][LPR];
-  __shared__ float2 stat[1024 / LPR];
-  const int lane = threadIdx.x, first = threadIdx.y, tid = first * LPR + lane;
-  // The attention kernel lets this one start once it has itself waited for the kernels before it, so the
-  // lengths can be read, and the slots found, while it runs.
-  if (tid < 32) plan_split(a, &sp, ctas, tid, false);
-  __syncthreads();
-  int id = blockIdx.x;  // ((l * B + b) * Hkv + h) * rows + r
-  const int r = id % a.rows;
-  id /= a.rows;
-  const int h = id % a.Hkv, lb = id / a.Hkv, b = lb % a.B, l = lb / a.B;
-  const int heads = a.Hkv * a.row_blocks, groups = sp.cum[b + 1] - sp.cum[b], share = sp.share;
-  const int rb = r / ROWS, n = r - rb * ROWS;
-  const int u0 = (l * sp.cum[a.B] + sp.cum[b]) * heads + (h * a.row_blocks + rb) * groups;
-  const int c0 = groups ? u0 / share : 0, c1 = groups ? (u0 + groups - 1) / share : 0;
-  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
-  pdl_trigger();
-  if (c0 == c1) return;  // written whole, or not valid
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float top = -INFINITY, lt = 0.f;
-  for (int c = c0 + first; c <= c1; c += 4 * blockDim.y) {
-    float2 ml[4];
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ci = c + i * (int)blockDim.y;
-      ml[i] = make_float2(-INFINITY, 0.f);
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ci <= c1) {  // (the first CTA's slot 1, unless its range begins with the unit)
-        const float* p = a.ws + (2 * (int64_t)ci + (ci > c0 || ci * share == u0 ? 0 : 1)) * slot_floats<D>(ROWS);
-        ml[i] = *reinterpret_cast<const float2*>(p + ROWS * D + 2 * n);
-        v[i] = *reinterpret_cast<const float4*>(p + n * D + 4 * lane);
-      }
-    }
-    const float m1 = fmaxf(top, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-    const float keep = top == -INFINITY ? 0.f : ex2(top - m1);
-    sum.x *= keep; sum.y *= keep; sum.z *= keep; sum.w *= keep;
-    lt *= keep;
-    top = m1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - top);
-      sum.x = fmaf(f, v[i].x, sum.x); sum.y = fmaf(f, v[i].y, sum.y);
-      sum.z = fmaf(f, v[i].z, sum.z); sum.w = fmaf(f, v[i].w, sum.w);
-      lt = fmaf(f, ml[i].y, lt);
-    }
-  }
-  part[first][lane] = sum;
-  if (lane == 0) stat[first] = make_float2(top, lt);
-  __syncthreads();
-  if (first == 0) {
-    top = -INFINITY;
-    for (int i = 0; i < (int)blockDim.y; ++i) top = fmaxf(top, stat[i].x);
-    sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    lt = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < (int)blockDim.y; ++i) {
-      const float2 ml = stat[i];
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      const float4 v = part[i][lane];
-      sum.x = fmaf(f, v.x, sum.x); sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z); sum.w = fmaf(f, v.w, sum.w);
-      lt = fmaf(f, ml.y, lt);
-    }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    const int64_t at = (((int64_t)lb * a.Hq + h * a.G) * a.nq + r) * D + 4 * lane;
-    store4(static_cast<T*>(a.o) + at, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
   }
 }
 
@@ -935,27 +700,28 @@ cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
   }
   e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), Lay::BYTES, s, a);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.L * a.B * a.Hkv * a.rows;
-  // slots of a unit if all are equally long: four for each lane of the merge
-  const int slots = a.ctas / (a.L * a.B * a.Hkv * a.row_blocks) + 2;
-  int at_once = 128 / (D / 4);
-  while (at_once < 1024 / (D / 4) && 4 * at_once < slots) at_once *= 2;
-  return launch_pdl(kv4_merge_kernel<D, NT, F32>, dim3((unsigned)rows), dim3(D / 4, at_once), 0, s, a, a.ctas);
+  return launch_kv4_merge<D, 8 * NT, typename std::conditional<F32, float, __nv_bfloat16>::type>(a, s);
 }
 
 }  // namespace
 
+// More than 16 query rows share a widened code often enough for the tensor-memory kernel (bf16; fp32
+// queries need their second fp16 term, and two weights for one, and stay here).
+static bool on_tensor_memory(const Kv4AttnArgs& a) { return a.dtype == STD_BF16 && a.rows > 16; }
+
 // Query rows of a block, and CTAs of an SM, by the kernel the call takes.
 void plan_kv4_attn(Kv4AttnArgs* a, int sms) {
-  const int nt = a->rows <= 8 ? 1 : 2;
-  a->row_blocks = (a->rows + 8 * nt - 1) / (8 * nt);
+  const bool tm = on_tensor_memory(*a);
+  const int block = tm ? kv4_attn_tc_rows() : a->rows <= 8 ? 8 : 16;
+  a->row_blocks = (a->rows + block - 1) / block;
   const int64_t tiles = (int64_t)a->L * a->B * a->Hkv * a->row_blocks * ((a->cap + kTile - 1) / kTile);
-  const int64_t most = (int64_t)sms * (nt == 1 && a->dtype == STD_BF16 ? 2 : 1);
+  const int64_t most = (int64_t)sms * (block == 8 && a->dtype == STD_BF16 ? 2 : 1);
   a->ctas = (int)(tiles < most ? tiles : most);
-  a->ws_floats = 2 * a->ctas * (int64_t)(8 * nt) * (a->d + 2);
+  a->ws_floats = 2 * a->ctas * (int64_t)block * (a->d + 2);
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
+  if (on_tensor_memory(a)) return launch_kv4_attn_tc(a, s);
   const bool one = a.rows <= 8, f32 = a.dtype == STD_F32;
   if (a.d == 128) {
     if (f32) return one ? launch<128, 1, true>(a, s) : launch<128, 2, true>(a, s);

@@ -1,0 +1,654 @@
+// Attention over a 4-bit K/V cache for more than 16 query rows of a KV head (verify rows): the
+// mathematics of kv4_attn.cu on the 5th-generation tensor cores.
+//
+// 64 query rows share each widened code here, so a tile's codes are widened once, into tensor and shared
+// memory, and both products run as tcgen05.mma with the keys (and then the channels) as their 128
+// rows and the query rows as their 64 columns:
+//   S_g^T [128 keys][64 rows] = K codes of group g (tensor memory) x Q_g (shared memory), g = 0, 1
+//   O_g^T [128 channels][64 rows] += V codes (shared memory, read transposed) x (P sv_g)^T (shared memory)
+// With keys in the lanes a key's scales and minima are a thread's own: it turns its column of S_0 and S_1
+// into logits and weights, multiplies them by sv_0 and sv_1 and writes 16-bit rows of the next operand.
+// (O_0 is valid for group 0's 64 channels, O_1 for group 1's: half of that product is thrown away, which
+// costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
+// reference of each row that moves only when some weight would leave fp16's range, so a tile has one
+// barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
+//
+// A tile at d = 128 is 18 KB; its two products are 768 clocks of the tensor cores, its 8,192 weights 512
+// clocks of the exponential unit and the widening and the weights together some 900 issue slots of
+// each scheduler; at full HBM rate it would be 760 clocks.
+#include "kv4_attn.cuh"
+
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+namespace stdb {
+namespace {
+
+constexpr int kRows = 64;               // query rows of a block
+constexpr int kShare = 16;              // rows of a thread: four threads a key
+constexpr int kThreads = kTile * kRows / kShare;
+constexpr int kStages = 4;
+constexpr int kFetcher = kThreads - 32;  // the thread that fetches tiles (thread 0 issues the products)
+constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
+constexpr float kSmall = 9.094947e-13f;
+constexpr float kHeadroom = 8.f;
+
+// Shared memory, from a 1024-byte boundary on: operands in 128-byte swizzled rows, then the ring of 4-bit
+// tiles, then tables.
+template <int D>
+struct Lay {
+  static constexpr int GR = D / kKv4Group;
+  static constexpr int V = 0;                             // [2][GR][128 keys][64 channels] fp16
+  static constexpr int V_GROUP = kTile * 128;
+  static constexpr int P = V + 4 * V_GROUP;               // [2][GR][128 keys][64 rows] fp16
+  static constexpr int P_GROUP = kTile * 128;
+  static constexpr int Q = P + 2 * GR * P_GROUP;          // [GR][64 rows][64 channels] fp16
+  static constexpr int Q_GROUP = kRows * 128;
+  static constexpr int RING = Q + GR * Q_GROUP;
+  static constexpr int TAB = RING + kStages * TileAt<D>::BYTES;
+  static constexpr int RED = TAB + 5 * kRows * 4;         // [4 warps][64 rows][3]
+  static constexpr int BYTES = RED + 4 * kRows * 3 * 4;
+};
+
+struct Ctl {
+  uint64_t full[kStages], s_done, pv_done[2];
+  Split split;
+  Fetch fetch;
+  uint32_t tmem;
+  float qmax[kThreads / 32];
+  volatile int abort;
+};
+
+// Tensor memory columns: K codes (two buffers of 32 columns a group), S (two buffers of one 64-column
+// accumulator a group), O (one a group).
+template <int D>
+struct Cols {
+  static constexpr int GR = D / kKv4Group;
+  static constexpr int K = 0, S = 2 * 32 * GR, O = S + 2 * kRows * GR;
+  static constexpr int N = 512;
+  static_assert(O + kRows * GR <= N, "tensor memory");
+};
+
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+// two codes as fp16 subnormals, c 2^-24 and c 2^-20 (kv4_attn.cu)
+__device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
+// two codes as c - 8: 0x6400 is 1024, whose last ten bits hold a code at bit 0 or bit 4
+__device__ __forceinline__ uint32_t centre0(uint32_t w) {
+  return as_u32(__hsub2(as_h2(widen0(w) | 0x64006400u), __float2half2_rn(1032.f)));
+}
+__device__ __forceinline__ uint32_t centre4(uint32_t w) {
+  return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 8 consecutive 32-bit columns of this thread's lane
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+// Position p of eight in an operand holds code (channel of the word) kPerm(p): the order in which masks
+// take codes out of a word, (0, 4), (1, 5), (2, 6), (3, 7); the second and fourth pair come at 2^-20.
+__device__ __forceinline__ int perm8(int p) { return (p >> 1) + 4 * (p & 1); }
+
+// One group of a thread's key of K to tensor memory (its lane), 32 columns.
+template <int D>
+__device__ __forceinline__ void widen_k(uint32_t row, uint32_t taddr, int gr) {
+  constexpr int GR = D / kKv4Group;
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 v = lds128(row + 16 * i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; k += GR) {
+      const uint32_t x = GR == 2 && gr ? w[k + GR - 1] : w[k];
+      const int j = 4 * ((4 * i + k) / GR);
+      r[j] = widen0(x);
+      r[j + 1] = widen4(x);
+      r[j + 2] = widen0(x >> 8);
+      r[j + 3] = widen4(x >> 8);
+    }
+  }
+  tc::tmem_st_x32(taddr, r);
+}
+
+// Half of a thread's key of V to its 128-byte rows of the operand, chunk c of 16 bytes at c ^ (key % 8).
+// The order of the 16-byte loads differs from lane to lane so that neither they nor the stores conflict.
+template <int D>
+__device__ __forceinline__ void widen_v(uint32_t row, uint32_t dst, int key, int part) {
+  constexpr int GR = D / kKv4Group;
+  const int a = (key >> 1) & 3, turn = ((a << 1) ^ (a >> 1) * 3) & 3;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const int c = D == 128 ? (2 * part + i) ^ turn : part ^ (turn & 1);
+    const uint4 v = lds128(row + 16 * c);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int gr = GR == 2 ? k & 1 : 0, chunk = GR == 2 ? 2 * c + (k >> 1) : 4 * c + k;
+      sts128(dst + gr * Lay<D>::V_GROUP + key * 128 + ((chunk ^ (key & 7)) << 4), centre0(w[k]), centre4(w[k]),
+             centre0(w[k] >> 8), centre4(w[k] >> 8));
+    }
+  }
+}
+
+// A block's queries: the operand (kRows x 64 for each group, fp16, scaled by a power of two, K-major with
+// swizzled rows), the group sums of the scaled queries and the factor that undoes the scaling.
+template <int D>
+__device__ __forceinline__ float load_queries(const Kv4AttnArgs& a, const Unit& u, int n0, Ctl* ctl, uint8_t* smem,
+                                              int tid) {
+  constexpr int GR = D / kKv4Group, NC = D / 8;  // channels of a thread: an eighth of a row
+  const int r = tid >> 3, part = tid & 7, row = u.rb * kRows + r;
+  float x[NC];
+  float top = 0.f;
+  const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + row) * D + part * NC;
+#pragma unroll
+  for (int i = 0; i < NC; i += 8) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < a.rows) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + i);
+    x[i] = lo_bf16(v.x); x[i + 1] = hi_bf16(v.x); x[i + 2] = lo_bf16(v.y); x[i + 3] = hi_bf16(v.y);
+    x[i + 4] = lo_bf16(v.z); x[i + 5] = hi_bf16(v.z); x[i + 6] = lo_bf16(v.w); x[i + 7] = hi_bf16(v.w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (fabsf(x[i + k]) < INFINITY) top = fmaxf(top, fabsf(x[i + k]));
+  }
+  top = warp_max(top);
+  if ((tid & 31) == 0) ctl->qmax[tid >> 5] = top;
+  __syncthreads();
+  top = warp_max(ctl->qmax[tid & (kThreads / 32 - 1)]);
+  int ex = (int)(__float_as_uint(top) >> 23) - 127;
+  ex = ex < -100 ? -100 : ex;
+  const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+  float back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)((ex > 100 ? ex - 10 : ex + 10) + 127) << 23);
+  if (ex > 100) back *= 1048576.f;
+  float sum = 0.f;
+  const int per = 8 / GR, gr = part / per, c0 = part % per * NC;  // threads of a group; channels of the group
+  uint8_t* base = smem + Lay<D>::Q + gr * Lay<D>::Q_GROUP + r * 128;
+#pragma unroll
+  for (int i = 0; i < NC; i += 8) {
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // pair k: channels k and k + 4 of the word
+      const float f = mul * (k & 1 ? 0.0625f : 1.f);
+      h[k] = as_u32(__floats2half2_rn(x[i + k] * f, x[i + k + 4] * f));
+      sum += (x[i + k] + x[i + k + 4]) * mul;
+    }
+    const int chunk = (c0 + i) >> 3;
+    *reinterpret_cast<uint4*>(base + ((chunk ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  sum *= 5.9604645e-8f;  // 2^-24
+#pragma unroll
+  for (int o = 1; o < 8 / GR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float* tab = reinterpret_cast<float*>(smem + Lay<D>::TAB);
+  if (part % per == 0) tab[gr * kRows + r] = sum;
+  if (part == 1) {
+    tab[2 * kRows + r] = INFINITY;  // minus the row's reference
+    reinterpret_cast<int*>(tab)[4 * kRows + r] = n0 + (row < a.rows ? row % a.nq : 0);  // keys it attends
+  }
+  return back;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnArgs a) {
+  using L = Lay<D>;
+  using C = Cols<D>;
+  using At = TileAt<D>;
+  constexpr int GR = D / kKv4Group;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl ctl;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sm = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int wg = warp >> 2, qd = warp & 3, key = tid & 127;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) tc::mbar_init(&ctl.full[s], 1);
+    tc::mbar_init(&ctl.s_done, 1);
+    tc::mbar_init(&ctl.pv_done[0], 1);
+    tc::mbar_init(&ctl.pv_done[1], 1);
+    ctl.abort = 0;
+    ctl.fetch.fills = ctl.fetch.left = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_wait();  // memory of earlier kernels in the stream is visible from here on
+  if (warp == 1) {
+    tc::tmem_alloc(&ctl.tmem, C::N);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0) plan_split(a, &ctl.split, gridDim.x, lane, blockIdx.x == 0);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  // (only now: a kernel that starts early must not take the tensor memory that this one has yet to get)
+  pdl_trigger();
+  const uint32_t tmem = ctl.tmem, lanes = tmem + ((uint32_t)(qd * 32) << 16);
+  const int total = ctl.split.total, share = ctl.split.share;
+  const int64_t begin64 = (int64_t)share * blockIdx.x;
+  const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
+  const uint32_t ring = sm + L::RING;
+  float* tab = reinterpret_cast<float*>(smem + L::TAB);  // sums of q (two groups), minus the references, factors
+  float* red = reinterpret_cast<float*>(smem + L::RED);
+  if (tid == kFetcher && begin < end) {
+    ctl.fetch.next = begin;
+    for (int s = 0; s < kStages; ++s) fetch_tile<D, kStages>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
+  }
+  // (start addresses are in units of 16 bytes and do not carry: shared memory is smaller than the field)
+  const uint64_t q_desc = tc::sdesc_sw128(sm + L::Q), v_desc = tc::sdesc_sw128_mn(sm + L::V, L::V_GROUP),
+                 p_desc = tc::sdesc_sw128_mn(sm + L::P, L::P_GROUP);
+  int tiles_read = 0;      // tiles of the units before this one
+  uint32_t s_count = 0;    // S products issued
+  uint32_t pv_count = 0;   // P V products issued, in turn on pv_done[0] and [1]
+  bool ok = true;
+
+  for (int t = begin; t < end && ok;) {
+    const Unit u = locate(a, ctl.split, t);
+    const int group = ctl.split.group, keys = keys_of(a, u.b), first = u.first * group;
+    const int n = min(u.groups - u.first, end - t);
+    const int nt = min(n * group, (keys + kTile - 1) / kTile - first);  // (may be none)
+    const int n0 = keys - a.nq + 1;
+    const float back = load_queries<D>(a, u, n0, &ctl, smem, tid);
+    f32x2 l[kShare / 2], pm[GR][kShare / 2];  // sums of p and of p (mv + 8 sv), two rows together
+#pragma unroll
+    for (int j = 0; j < kShare / 2; ++j) {
+      l[j] = f2_make(0.f, 0.f);
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_make(0.f, 0.f);
+    }
+    const uint32_t pv0 = pv_count;
+
+    auto stage_of = [&](int i) { return ring + (uint32_t)((tiles_read + i) % kStages) * At::BYTES; };
+    auto wait_tile = [&](int i) {
+      const int k = tiles_read + i;
+      return tc::mbar_wait_warp(&ctl.full[k % kStages], (uint32_t)(k / kStages) & 1u, &ctl.abort, a.err);
+    };
+    // the P V product `c` (counted from the kernel's start) has finished
+    auto wait_pv = [&](uint32_t c) {
+      return tc::mbar_wait_warp(&ctl.pv_done[c & 1], (c >> 1) & 1u, &ctl.abort, a.err);
+    };
+    // One thread issues the products, 24 of them for a tile: the descriptors are sums of constants and
+    // a few bases, as each instruction on the way is latency (worked out one by one they took 3,000 clocks).
+    auto issue_s = [&](int i) {  // S_g = K codes of tile i x Q_g
+      constexpr uint32_t id = idesc_f16(128, kRows);
+      const uint32_t d = tmem + C::S + (i & 1) * GR * kRows, k0 = tmem + C::K + (i & 1) * GR * 32;
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::umma_bf16_ts(d + gr * kRows, k0 + gr * 32 + 8 * k, q_desc + (gr * L::Q_GROUP + 32 * k) / 16, id,
+                           k > 0 ? 1u : 0u);
+      tc::umma_commit(&ctl.s_done);
+    };
+    auto issue_pv = [&](int i, uint32_t c) {  // O_g += V codes x (P sv_g), buffers c % 2
+      constexpr uint32_t id = idesc_f16(128, kRows) | (1u << 15) | (1u << 16);  // both read across their rows
+      const uint64_t v = v_desc + (c & 1) * (2 * L::V_GROUP / 16), p = p_desc + (c & 1) * (GR * L::P_GROUP / 16);
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::umma_bf16(tmem + C::O + gr * kRows, v + k * 128, p + gr * (L::P_GROUP / 16) + k * 128, id,
+                        i > 0 || k > 0 ? 1u : 0u);
+      tc::umma_commit(&ctl.pv_done[c & 1]);
+    };
+
+    // threads of K: wg 0 (group 0) and 3 (group 1); of V: 1 and 2, half a row each
+    const bool k_side = wg == 0 || (GR == 2 && wg == 3);
+    if (nt > 0) {
+      ok = wait_tile(0);
+      if (ok && k_side) {
+        widen_k<D>(stage_of(0) + key * At::CW, lanes + C::K + (wg == 3 ? 32 : 0), wg == 3);
+        tc::tmem_st_wait();
+      }
+    }
+    tc::fence_proxy_async();  // (the queries)
+    tc::fence_before_sync();
+    if (__syncthreads_or(!ok || ctl.abort)) {
+      ok = false;
+      break;
+    }
+    if (tid == 0 && nt > 0) {
+      tc::fence_after_sync();
+      issue_s(0);
+    }
+    if (nt > 0) ++s_count;
+
+    for (int i = 0; i < nt; ++i) {
+      const uint32_t cur = stage_of(i);
+      const uint32_t buf = pv_count & 1;
+      // widen the next tile's K and this tile's V
+      if (i + 1 < nt) {
+        ok = ok && wait_tile(i + 1);
+        if (ok && k_side) {
+          widen_k<D>(stage_of(i + 1) + key * At::CW, lanes + C::K + ((i + 1) & 1) * GR * 32 + (wg == 3 ? 32 : 0), wg == 3);
+          tc::tmem_st_wait();
+        }
+      }
+      if (pv_count >= 2) ok = ok && wait_pv(pv_count - 2);  // the buffers' last readers
+      if (ok && (wg == 1 || wg == 2))
+        widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * 2 * L::V_GROUP, key, wg - 1);
+
+      // this thread's key: scales (K's with the factor that undoes the queries'), position
+      const int pos = (first + i) * kTile + key;
+      float sk[GR], mk[GR], sv[GR], mv[GR], smax = kSmall;
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) {
+        const uint32_t uk = *reinterpret_cast<const uint32_t*>(smem + (cur - sm) + At::KS + key * At::SW + 4 * gr);
+        const uint32_t uv = *reinterpret_cast<const uint32_t*>(smem + (cur - sm) + At::VS + key * At::SW + 4 * gr);
+        const bool in = pos < keys;  // (past the last key the bytes may be anything)
+        sk[gr] = in ? lo_bf16(uk) * back : 0.f;
+        mk[gr] = in ? hi_bf16(uk) * back : 0.f;
+        sv[gr] = in ? lo_bf16(uv) : 0.f;
+        mv[gr] = in ? fmaf(8.f, lo_bf16(uv), hi_bf16(uv)) : 0.f;
+        smax = fmaxf(smax, sv[gr]);
+      }
+      const bool edge = (first + i + 1) * kTile > n0;  // some query position does not attend some key of the tile
+      ok = ok && tc::mbar_wait_warp(&ctl.s_done, (s_count - 1) & 1u, &ctl.abort, a.err);
+      tc::fence_after_sync();
+
+      const uint32_t s_at = lanes + C::S + (i & 1) * GR * kRows + wg * kShare;
+      const uint32_t p_at = sm + L::P + buf * GR * L::P_GROUP + key * 128;
+      f32x2 p[kShare / 2];
+      // Weights and the operand's rows.  Where some weight leaves fp16's range (the first tile of a unit, as
+      // no reference is set yet, and rarely after it) the references move and it is done once more.
+      for (bool moved = false;;) {
+        float big = 0.f;
+        if (ok) {
+#pragma unroll
+          for (int h0 = 0; h0 < kShare; h0 += 8) {
+            uint32_t s[GR][8];
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) tmem_ld_x8(s_at + gr * kRows + h0, s[gr]);
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) tmem_ld_wait8(s[gr]);
+            f32x2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {  // rows 2 k .. 2 k + 3
+              const int row = wg * kShare + h0 + 2 * k;
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(tab + 2 * kRows + row);
+              const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(tab + row);
+              x[k] = f2_fma(f2_make(mk[0], mk[0]), q0.x, m.x);
+              x[k + 1] = f2_fma(f2_make(mk[0], mk[0]), q0.y, m.y);
+              if constexpr (GR == 2) {
+                const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(tab + kRows + row);
+                x[k] = f2_fma(f2_make(mk[1], mk[1]), q1.x, x[k]);
+                x[k + 1] = f2_fma(f2_make(mk[1], mk[1]), q1.y, x[k + 1]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr)
+                x[k] = f2_fma(f2_make(sk[gr], sk[gr]),
+                              f2_make(__uint_as_float(s[gr][2 * k]), __uint_as_float(s[gr][2 * k + 1])), x[k]);
+            if (edge) {
+              const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare + h0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float x0, x1;
+                f2_split(x[k], x0, x1);
+                x[k] = f2_make(pos < lim[2 * k] ? x0 : -INFINITY, pos < lim[2 * k + 1] ? x1 : -INFINITY);
+              }
+            }
+            uint32_t pk[GR][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x0, x1;
+              f2_split(x[k], x0, x1);
+              const f32x2 pp = f2_make(ex2(x0), ex2(x1));
+              p[h0 / 2 + k] = pp;
+              float w0, w1;
+              f2_split(f2_mul(pp, f2_make(smax, smax)), w0, w1);
+              big = max3f(big, w0, w1);
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr) {
+                f2_split(f2_mul(pp, f2_make(sv[gr], sv[gr])), w0, w1);
+                pk[gr][k] = as_u32(__floats2half2_rn(w0, w1));
+              }
+            }
+            const int chunk = (wg * kShare + h0) / 8;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+              sts128(p_at + gr * L::P_GROUP + ((chunk ^ (key & 7)) << 4), pk[gr][0], pk[gr][1], pk[gr][2], pk[gr][3]);
+          }
+        }
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        if (!__syncthreads_or((!moved && !(big <= kLimit)) || !ok || ctl.abort)) break;
+        if (ok && pv_count > pv0) ok = wait_pv(pv_count - 1);  // O is still
+        if (__syncthreads_or(!ok || ctl.abort)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        moved = true;
+        // every row's largest logit + log2 of the key's scale, first over the warps
+        const float ls = __log2f(smax);
+#pragma unroll 1
+        for (int r = 0; r < kShare; r += 4) {
+          uint32_t s[GR][4];
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_x4(s_at + gr * kRows + r, s[gr]);
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_wait4(s[gr]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = wg * kShare + r + k;
+            float x = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), fmaf(mk[gr], tab[gr * kRows + row], x));
+            const float z = warp_max(pos < reinterpret_cast<const int*>(tab)[4 * kRows + row] ? x + ls : -INFINITY);
+            if (lane == 0) red[qd * kRows + row] = z;
+          }
+        }
+        __syncthreads();
+        if (tid < kRows) {
+          const float z = fmaxf(fmaxf(red[tid], red[kRows + tid]), fmaxf(red[2 * kRows + tid], red[3 * kRows + tid]));
+          const float m0 = -tab[2 * kRows + tid];
+          float f = 1.f;
+          if (z - m0 > 14.9f) {
+            f = ex2(m0 - (z - kHeadroom));
+            tab[2 * kRows + tid] = kHeadroom - z;
+          }
+          tab[3 * kRows + tid] = f;
+        }
+        __syncthreads();
+        const f32x2* f = reinterpret_cast<const f32x2*>(tab + 3 * kRows + wg * kShare);
+#pragma unroll
+        for (int j = 0; j < kShare / 2; ++j) {
+          l[j] = f2_mul(l[j], f[j]);
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_mul(pm[gr][j], f[j]);
+        }
+        if (pv_count > pv0) {
+          // this thread's channel, in the accumulator that is valid for it
+          const uint32_t o_at = lanes + C::O + (GR == 2 ? (qd >> 1) * kRows : 0) + wg * kShare;
+          uint32_t o[16];
+          tc::tmem_ld_x16(o_at, o);
+          tc::tmem_ld_wait16(o);
+#pragma unroll
+          for (int j = 0; j < kShare; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * tab[3 * kRows + wg * kShare + j]);
+          tc::tmem_st_x16(o_at, o);
+          tc::tmem_st_wait();
+        }
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < kShare / 2; ++j) {
+        l[j] = f2_add(l[j], p[j]);
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) {
+          f32x2 q = f2_fma(p[j], f2_make(mv[gr], mv[gr]), pm[gr][j]);
+          if (edge && mv[gr] != mv[gr]) {  // a row that is not finite, and query positions that do not attend it
+            const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare + 2 * j;
+            float q0, q1, b0, b1;
+            f2_split(q, q0, q1);
+            f2_split(pm[gr][j], b0, b1);
+            q = f2_make(pos < lim[0] ? q0 : b0, pos < lim[1] ? q1 : b1);
+          }
+          pm[gr][j] = q;
+        }
+      }
+      if (tid == 0) {
+        tc::fence_after_sync();
+        if (i + 1 < nt) issue_s(i + 1);
+        issue_pv(i, pv_count);
+      } else if (tid == kFetcher) {
+        fetch_tile<D, kStages>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);  // into this tile's stage
+      }
+      if (i + 1 < nt) ++s_count;
+      ++pv_count;
+    }
+    if (!ok) break;
+    tiles_read += nt > 0 ? nt : 0;
+
+    // Sums over the keys: the two half-warps, then 16 rows over 16 lanes (each step halves the rows a lane
+    // holds), then the warps.
+    if (nt > 0) ok = wait_pv(pv_count - 1);
+    tc::fence_after_sync();
+    auto scatter = [&](const f32x2 (&pairs)[kShare / 2]) {
+      float v[kShare];
+#pragma unroll
+      for (int k = 0; k < kShare; ++k) {
+        float a0, a1;
+        f2_split(pairs[k / 2], a0, a1);
+        v[k] = k & 1 ? a1 : a0;
+        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+      }
+#pragma unroll
+      for (int w = kShare / 2; w >= 1; w >>= 1) {
+        const bool up = (lane & w) != 0;
+#pragma unroll
+        for (int k = 0; k < kShare / 2; ++k) {
+          if (k < w) {
+            const float give = up ? v[k] : v[k + w], keep = up ? v[k + w] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+          }
+        }
+      }
+      return v[0];
+    };
+    {
+      float* mine = red + (qd * kRows + wg * kShare + (lane & 15)) * 3;
+      const float sl = scatter(l);
+      if (lane < 16) mine[0] = sl;
+#pragma unroll
+      for (int gr = 0; gr < GR; ++gr) {
+        const float sp = scatter(pm[gr]);
+        if (lane < 16) mine[1 + gr] = sp;
+      }
+    }
+    if (__syncthreads_or(!ok || ctl.abort)) {
+      ok = false;
+      break;
+    }
+    {
+      const bool whole = n == u.groups;
+      float* slot = nullptr;
+      if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(kRows);
+      const int m = qd * 32 + lane, gr = GR == 2 ? qd >> 1 : 0;  // accumulator lane: channel of the group, permuted
+      const int ch = (GR == 2 ? 64 * gr : 0) + (m & 56 & (GR == 2 ? 63 : 127)) + perm8(m & 7);
+      uint32_t o[16];
+      if (nt > 0) {
+        tc::tmem_ld_x16(lanes + C::O + gr * kRows + wg * kShare, o);
+        tc::tmem_ld_wait16(o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kShare; ++j) o[j] = 0;
+      }
+      const bool mine = ch < D && (GR == 2 || m < 64);
+#pragma unroll
+      for (int j = 0; j < kShare; ++j) {
+        const int row = wg * kShare + j, r = u.rb * kRows + row;
+        if (r >= a.rows) break;
+        float sl = 0.f, sp = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          sl += red[(w * kRows + row) * 3];
+          sp += red[(w * kRows + row) * 3 + 1 + gr];
+        }
+        const float v = __uint_as_float(o[j]) + sp;
+        if (whole) {
+          const float inv = sl == 0.f ? 0.f : 1.f / sl;  // a row that attends no key: zeros
+          const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + ch;
+          if (mine) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v * inv);
+        } else if (mine) {
+          slot[row * D + ch] = v;
+          if (ch == 0)
+            *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(-tab[2 * kRows + row], sl);
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncthreads();  // tables and accumulators are free for the next unit
+    tc::fence_after_sync();
+    t += n;
+  }
+
+  if (!ok) {  // what is in flight lands in this CTA's memory: wait for it
+    __syncthreads();
+    if (tid == 0) {
+      volatile int none = 0;
+      for (int k = max(0, ctl.fetch.fills - kStages); k < ctl.fetch.fills; ++k)
+        tc::mbar_wait(&ctl.full[k % kStages], (uint32_t)(k / kStages) & 1u, &none, a.err);
+      if (pv_count > 0) tc::mbar_wait(&ctl.pv_done[(pv_count - 1) & 1], ((pv_count - 1) >> 1) & 1u, &none, a.err);
+      if (s_count > 0) tc::mbar_wait(&ctl.s_done, (s_count - 1) & 1u, &none, a.err);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, C::N);
+}
+
+template <int D>
+cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
+  auto* kern = kv4_attn_tc_kernel<D>;
+  constexpr int bytes = Lay<D>::BYTES + 1024;
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use its shared memory
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), bytes, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_kv4_merge<D, kRows, __nv_bfloat16>(a, s);
+}
+
+}  // namespace
+
+int kv4_attn_tc_rows() { return kRows; }
+
+cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, cudaStream_t s) {
+  return a.d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}
+
+}  // namespace stdb
