@@ -2,14 +2,13 @@
 // mathematics of kv4_attn.cu on the 5th-generation tensor cores.
 //
 // 64 query rows share each widened code here, so a tile's codes are widened once, into tensor and shared
-// memory, and both products run as tcgen05.mma with the keys (and then the channels) as their 128
-// rows and the query rows as their 64 columns:
+// memory, and both products run as tcgen05.mma:
 //   S_g^T [128 keys][64 rows] = K codes of group g (tensor memory) x Q_g (shared memory), g = 0, 1
-//   O_g^T [128 channels][64 rows] += V codes (shared memory, read transposed) x (P sv_g)^T (shared memory)
-// With keys in the lanes a key's scales and minima are a thread's own: it turns its column of S_0 and S_1
+//   O [2 x 64 rows][128 channels] += (P sv_0 over P sv_1) x V codes (both shared memory, read across their rows)
+// With keys in the lanes of S a key's scales and minima are a thread's own: it turns its part of S_0 and S_1
 // into logits and weights, multiplies them by sv_0 and sv_1 and writes 16-bit rows of the next operand.
-// (O_0 is valid for group 0's 64 channels, O_1 for group 1's: half of that product is thrown away, which
-// costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
+// (O's upper 64 rows are valid for group 0's channels, the lower for group 1's: half of the product is
+// thrown away, which costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
 // reference of each row that moves only when some weight would leave fp16's range, so a tile has one
 // barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
 //
@@ -29,7 +28,7 @@ constexpr int kRows = 64;               // query rows of a block
 constexpr int kShare = 16;              // rows of a thread: four threads a key
 constexpr int kThreads = kTile * kRows / kShare;
 constexpr int kStages = 4;
-constexpr int kFetcher = kThreads - 32;  // the thread that fetches tiles (thread 0 issues the products)
+constexpr int kFetcher = kThreads - 32;  // the thread that fetches tiles (warp 0 issues the products)
 constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
 constexpr float kSmall = 9.094947e-13f;
 constexpr float kHeadroom = 8.f;
@@ -41,9 +40,9 @@ struct Lay {
   static constexpr int GR = D / kKv4Group;
   static constexpr int V = 0;                             // [2][GR][128 keys][64 channels] fp16
   static constexpr int V_GROUP = kTile * 128;
-  static constexpr int P = V + 4 * V_GROUP;               // [2][GR][128 keys][64 rows] fp16
+  static constexpr int P = V + 2 * GR * V_GROUP;          // [2][2][128 keys][64 rows] fp16 (one group: the second unused)
   static constexpr int P_GROUP = kTile * 128;
-  static constexpr int Q = P + 2 * GR * P_GROUP;          // [GR][64 rows][64 channels] fp16
+  static constexpr int Q = P + 4 * P_GROUP;          // [GR][64 rows][64 channels] fp16
   static constexpr int Q_GROUP = kRows * 128;
   static constexpr int RING = Q + GR * Q_GROUP;
   static constexpr int TAB = RING + kStages * TileAt<D>::BYTES;
@@ -61,13 +60,13 @@ struct Ctl {
 };
 
 // Tensor memory columns: K codes (two buffers of 32 columns a group), S (two buffers of one 64-column
-// accumulator a group), O (one a group).
+// accumulator a group), O (a column a channel).
 template <int D>
 struct Cols {
   static constexpr int GR = D / kKv4Group;
   static constexpr int K = 0, S = 2 * 32 * GR, O = S + 2 * kRows * GR;
   static constexpr int N = 512;
-  static_assert(O + kRows * GR <= N, "tensor memory");
+  static_assert(O + D <= N, "tensor memory");
 };
 
 constexpr uint32_t idesc_f16(int M, int N) {
@@ -100,6 +99,28 @@ __device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// tcgen05.mma and its commit by the lane whose `leader` is set; the other operands are the warp's.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a_tmem), "l"(b), "r"(id), "r"(add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+      ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
 // 8 consecutive 32-bit columns of this thread's lane
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -115,7 +136,7 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
 
 // Position p of eight in an operand holds code (channel of the word) kPerm(p): the order in which masks
 // take codes out of a word, (0, 4), (1, 5), (2, 6), (3, 7); the second and fourth pair come at 2^-20.
-__device__ __forceinline__ int perm8(int p) { return (p >> 1) + 4 * (p & 1); }
+__device__ __forceinline__ constexpr int perm8(int p) { return (p >> 1) + 4 * (p & 1); }
 
 // One group of a thread's key of K to tensor memory (its lane), 32 columns.
 template <int D>
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   tc::fence_after_sync();
   // (only now: a kernel that starts early must not take the tensor memory that this one has yet to get)
   pdl_trigger();
-  const uint32_t tmem = ctl.tmem, lanes = tmem + ((uint32_t)(qd * 32) << 16);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0), lanes = tmem + ((uint32_t)(qd * 32) << 16);
   const int total = ctl.split.total, share = ctl.split.share;
   const int64_t begin64 = (int64_t)share * blockIdx.x;
   const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
@@ -259,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     ctl.fetch.next = begin;
     for (int s = 0; s < kStages; ++s) fetch_tile<D, kStages>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
   }
+  uint32_t leader;  // one lane of each warp
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(leader));
   // (start addresses are in units of 16 bytes and do not carry: shared memory is smaller than the field)
   const uint64_t q_desc = tc::sdesc_sw128(sm + L::Q), v_desc = tc::sdesc_sw128_mn(sm + L::V, L::V_GROUP),
                  p_desc = tc::sdesc_sw128_mn(sm + L::P, L::P_GROUP);
@@ -292,29 +315,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     auto wait_pv = [&](uint32_t c) {
       return tc::mbar_wait_warp(&ctl.pv_done[c & 1], (c >> 1) & 1u, &ctl.abort, a.err);
     };
-    // One thread issues the products, 24 of them for a tile: the descriptors are sums of constants and
-    // a few bases, as each instruction on the way is latency (worked out one by one they took 3,000 clocks).
+    // The whole of warp 0 comes here and one lane issues, so that addresses and descriptors are the warp's
+    // and not a lane's: a tcgen05.mma takes them from uniform registers, and a lane's own have to be moved
+    // there first (16 products of a tile: 1,750 clocks that way).
     auto issue_s = [&](int i) {  // S_g = K codes of tile i x Q_g
       constexpr uint32_t id = idesc_f16(128, kRows);
-      const uint32_t d = tmem + C::S + (i & 1) * GR * kRows, k0 = tmem + C::K + (i & 1) * GR * 32;
+      const uint32_t odd = __shfl_sync(0xffffffffu, i & 1, 0);
+      const uint32_t d = tmem + C::S + odd * GR * kRows, k0 = tmem + C::K + odd * GR * 32;
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc::umma_bf16_ts(d + gr * kRows, k0 + gr * 32 + 8 * k, q_desc + (gr * L::Q_GROUP + 32 * k) / 16, id,
-                           k > 0 ? 1u : 0u);
-      tc::umma_commit(&ctl.s_done);
+          mma_ts(leader, d + gr * kRows, k0 + gr * 32 + 8 * k, q_desc + (gr * L::Q_GROUP + 32 * k) / 16, id, k > 0);
+      commit(leader, &ctl.s_done);
     };
-    auto issue_pv = [&](int i, uint32_t c) {  // O_g += V codes x (P sv_g), buffers c % 2
-      constexpr uint32_t id = idesc_f16(128, kRows) | (1u << 15) | (1u << 16);  // both read across their rows
-      const uint64_t v = v_desc + (c & 1) * (2 * L::V_GROUP / 16), p = p_desc + (c & 1) * (GR * L::P_GROUP / 16);
+    auto issue_pv = [&](int i, uint32_t c) {  // O += (P sv_g) x V codes, buffers c % 2
+      constexpr uint32_t id = idesc_f16(128, D) | (1u << 15) | (1u << 16);  // both read across their rows
+      const uint32_t odd = __shfl_sync(0xffffffffu, c & 1, 0), old = __shfl_sync(0xffffffffu, i > 0 ? 1 : 0, 0);
+      const uint64_t v = v_desc + odd * (GR * L::V_GROUP / 16), p = p_desc + odd * (2 * L::P_GROUP / 16);
 #pragma unroll
-      for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::umma_bf16(tmem + C::O + gr * kRows, v + k * 128, p + gr * (L::P_GROUP / 16) + k * 128, id,
-                        i > 0 || k > 0 ? 1u : 0u);
-      tc::umma_commit(&ctl.pv_done[c & 1]);
+      for (int k = 0; k < 8; ++k) mma_ss(leader, tmem + C::O, p + k * 128, v + k * 128, id, k > 0 ? 1u : old);
+      commit(leader, &ctl.pv_done[odd]);
     };
 
     // threads of K: wg 0 (group 0) and 3 (group 1); of V: 1 and 2, half a row each
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       ok = false;
       break;
     }
-    if (tid == 0 && nt > 0) {
+    if (warp == 0 && nt > 0) {
       tc::fence_after_sync();
       issue_s(0);
     }
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       }
       if (pv_count >= 2) ok = ok && wait_pv(pv_count - 2);  // the buffers' last readers
       if (ok && (wg == 1 || wg == 2))
-        widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * 2 * L::V_GROUP, key, wg - 1);
+        widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * GR * L::V_GROUP, key, wg - 1);
 
       // this thread's key: scales (K's with the factor that undoes the queries'), position
       const int pos = (first + i) * kTile + key;
@@ -372,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       tc::fence_after_sync();
 
       const uint32_t s_at = lanes + C::S + (i & 1) * GR * kRows + wg * kShare;
-      const uint32_t p_at = sm + L::P + buf * GR * L::P_GROUP + key * 128;
+      const uint32_t p_at = sm + L::P + buf * 2 * L::P_GROUP + key * 128;
       f32x2 p[kShare / 2];
       // Weights and the operand's rows.  Where some weight leaves fp16's range (the first tile of a unit, as
       // no reference is set yet, and rarely after it) the references move and it is done once more.
@@ -486,35 +507,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_mul(pm[gr][j], f[j]);
         }
         if (pv_count > pv0) {
-          // this thread's channel, in the accumulator that is valid for it
-          const uint32_t o_at = lanes + C::O + (GR == 2 ? (qd >> 1) * kRows : 0) + wg * kShare;
-          uint32_t o[16];
-          tc::tmem_ld_x16(o_at, o);
-          tc::tmem_ld_wait16(o);
+          // this thread's row (lane) of O, a quarter of its group's channels
+          const float fr = tab[3 * kRows + (key & 63)];
+          if (GR == 2 || key < 64) {
+            const uint32_t o_at = lanes + C::O + (key < 64 ? 0 : 64) + wg * 16;
+            uint32_t o[16];
+            tc::tmem_ld_x16(o_at, o);
+            tc::tmem_ld_wait16(o);
 #pragma unroll
-          for (int j = 0; j < kShare; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * tab[3 * kRows + wg * kShare + j]);
-          tc::tmem_st_x16(o_at, o);
-          tc::tmem_st_wait();
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fr);
+            tc::tmem_st_x16(o_at, o);
+            tc::tmem_st_wait();
+          }
         }
       }
       if (!ok) break;
+      if (edge && (mv[0] != mv[0] || mv[GR - 1] != mv[GR - 1])) {
+        // a row that is not finite: query positions that do not attend it must not multiply by it
+        const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare;
 #pragma unroll
-      for (int j = 0; j < kShare / 2; ++j) {
-        l[j] = f2_add(l[j], p[j]);
+        for (int j = 0; j < kShare / 2; ++j) {
+          float p0, p1;
+          f2_split(p[j], p0, p1);
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          f32x2 q = f2_fma(p[j], f2_make(mv[gr], mv[gr]), pm[gr][j]);
-          if (edge && mv[gr] != mv[gr]) {  // a row that is not finite, and query positions that do not attend it
-            const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare + 2 * j;
-            float q0, q1, b0, b1;
-            f2_split(q, q0, q1);
-            f2_split(pm[gr][j], b0, b1);
-            q = f2_make(pos < lim[0] ? q0 : b0, pos < lim[1] ? q1 : b1);
-          }
-          pm[gr][j] = q;
+          for (int gr = 0; gr < GR; ++gr)
+            pm[gr][j] = f2_add(pm[gr][j], f2_make(pos < lim[2 * j] ? p0 * mv[gr] : 0.f,
+                                                  pos < lim[2 * j + 1] ? p1 * mv[gr] : 0.f));
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kShare / 2; ++j)
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_fma(p[j], f2_make(mv[gr], mv[gr]), pm[gr][j]);
       }
-      if (tid == 0) {
+#pragma unroll
+      for (int j = 0; j < kShare / 2; ++j) l[j] = f2_add(l[j], p[j]);
+      if (warp == 0) {
         tc::fence_after_sync();
         if (i + 1 < nt) issue_s(i + 1);
         issue_pv(i, pv_count);
@@ -571,36 +599,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       const bool whole = n == u.groups;
       float* slot = nullptr;
       if (!whole) slot = a.ws + (2 * (int64_t)blockIdx.x + (t == begin ? 0 : 1)) * slot_floats<D>(kRows);
-      const int m = qd * 32 + lane, gr = GR == 2 ? qd >> 1 : 0;  // accumulator lane: channel of the group, permuted
-      const int ch = (GR == 2 ? 64 * gr : 0) + (m & 56 & (GR == 2 ? 63 : 127)) + perm8(m & 7);
+      // this thread's row of O (the lanes of both groups' halves) and a quarter of the group's channels
+      const int row = key & 63, gr = key >> 6, r = u.rb * kRows + row, c0 = 64 * gr + 16 * wg;
       uint32_t o[16];
       if (nt > 0) {
-        tc::tmem_ld_x16(lanes + C::O + gr * kRows + wg * kShare, o);
+        tc::tmem_ld_x16(lanes + C::O + c0, o);
         tc::tmem_ld_wait16(o);
       } else {
 #pragma unroll
-        for (int j = 0; j < kShare; ++j) o[j] = 0;
+        for (int j = 0; j < 16; ++j) o[j] = 0;
       }
-      const bool mine = ch < D && (GR == 2 || m < 64);
-#pragma unroll
-      for (int j = 0; j < kShare; ++j) {
-        const int row = wg * kShare + j, r = u.rb * kRows + row;
-        if (r >= a.rows) break;
+      if (r < a.rows && gr < GR) {
         float sl = 0.f, sp = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           sl += red[(w * kRows + row) * 3];
           sp += red[(w * kRows + row) * 3 + 1 + gr];
         }
-        const float v = __uint_as_float(o[j]) + sp;
+        const float inv = sl == 0.f ? 0.f : 1.f / sl;  // a row that attends no key: zeros
+        float v[16];  // in the channels' order
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[(j & 8) + perm8(j & 7)] = __uint_as_float(o[j]) + sp;
         if (whole) {
-          const float inv = sl == 0.f ? 0.f : 1.f / sl;  // a row that attends no key: zeros
-          const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + ch;
-          if (mine) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v * inv);
-        } else if (mine) {
-          slot[row * D + ch] = v;
-          if (ch == 0)
-            *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(-tab[2 * kRows + row], sl);
+          const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + c0;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at;
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            store4(out + j, make_float4(v[j] * inv, v[j + 1] * inv, v[j + 2] * inv, v[j + 3] * inv));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(slot + row * D + c0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          if (c0 == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(-tab[2 * kRows + row], sl);
         }
       }
     }
