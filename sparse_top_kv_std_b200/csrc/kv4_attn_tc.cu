@@ -28,7 +28,10 @@ constexpr int kRows = 64;               // query rows of a block
 constexpr int kShare = 16;              // rows of a thread: four threads a key
 constexpr int kThreads = kTile * kRows / kShare;
 constexpr int kStages = 4;
-constexpr int kFetcher = kThreads - 32;  // the thread that fetches tiles (warp 0 issues the products)
+// The thread that fetches tiles, and the warps that issue the products: of those that widen K, which is less
+// work than V.  (The issue of P V blocks its warp until the tensor cores have taken most of it, some 800
+// clocks; wg 3 has the fewest rows where a block is short.)
+constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 12;
 constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
 constexpr float kSmall = 9.094947e-13f;
 constexpr float kHeadroom = 8.f;
@@ -85,6 +88,11 @@ __device__ __forceinline__ uint32_t centre0(uint32_t w) {
 __device__ __forceinline__ uint32_t centre4(uint32_t w) {
   return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -120,6 +128,14 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
       ::"r"(smem_u32(bar)), "r"(leader)
       : "memory");
+}
+// Wait for a phase, by a whole warp.  A wait that gives up raises the CTA's abort flag and the warp goes on,
+// within its own buffers, to the next barrier, where every thread sees the flag.
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  if (!__all_sync(0xffffffffu, tc::mbar_try_wait(smem_u32(bar), parity))) {
+    tc::mbar_wait(bar, parity, abort, err);
+    __syncwarp();
+  }
 }
 // 8 consecutive 32-bit columns of this thread's lane
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -166,11 +182,13 @@ template <int D>
 __device__ __forceinline__ void widen_v(uint32_t row, uint32_t dst, int key, int part) {
   constexpr int GR = D / kKv4Group;
   const int a = (key >> 1) & 3, turn = ((a << 1) ^ (a >> 1) * 3) & 3;
+  uint4 v[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) v[i] = lds128(row + 16 * (D == 128 ? (2 * part + i) ^ turn : part ^ (turn & 1)));
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
     const int c = D == 128 ? (2 * part + i) ^ turn : part ^ (turn & 1);
-    const uint4 v = lds128(row + 16 * c);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int gr = GR == 2 ? k & 1 : 0, chunk = GR == 2 ? 2 * c + (k >> 1) : 4 * c + k;
@@ -306,16 +324,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     }
     const uint32_t pv0 = pv_count;
 
+    const int live = min(kRows, a.rows - u.rb * kRows);  // rows of the block
     auto stage_of = [&](int i) { return ring + (uint32_t)((tiles_read + i) % kStages) * At::BYTES; };
     auto wait_tile = [&](int i) {
       const int k = tiles_read + i;
-      return tc::mbar_wait_warp(&ctl.full[k % kStages], (uint32_t)(k / kStages) & 1u, &ctl.abort, a.err);
+      wait_for(&ctl.full[k % kStages], (uint32_t)(k / kStages) & 1u, &ctl.abort, a.err);
     };
     // the P V product `c` (counted from the kernel's start) has finished
-    auto wait_pv = [&](uint32_t c) {
-      return tc::mbar_wait_warp(&ctl.pv_done[c & 1], (c >> 1) & 1u, &ctl.abort, a.err);
-    };
-    // The whole of warp 0 comes here and one lane issues, so that addresses and descriptors are the warp's
+    auto wait_pv = [&](uint32_t c) { wait_for(&ctl.pv_done[c & 1], (c >> 1) & 1u, &ctl.abort, a.err); };
+    // A whole warp comes here and one lane issues, so that addresses and descriptors are the warp's
     // and not a lane's: a tcgen05.mma takes them from uniform registers, and a lane's own have to be moved
     // there first (16 products of a tile: 1,750 clocks that way).
     auto issue_s = [&](int i) {  // S_g = K codes of tile i x Q_g
@@ -338,89 +355,94 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       commit(leader, &ctl.pv_done[odd]);
     };
 
-    // threads of K: wg 0 (group 0) and 3 (group 1); of V: 1 and 2, half a row each
+    // Threads that widen K: wg 0 (group 0) and 3 (group 1); V: 1 and 2, half a row each.
     const bool k_side = wg == 0 || (GR == 2 && wg == 3);
-    if (nt > 0) {
-      ok = wait_tile(0);
-      if (ok && k_side) {
-        widen_k<D>(stage_of(0) + key * At::CW, lanes + C::K + (wg == 3 ? 32 : 0), wg == 3);
+    auto widen_keys = [&](int i) {
+      if (k_side) {
+        widen_k<D>(stage_of(i) + key * At::CW, lanes + C::K + (i & 1) * GR * 32 + (wg == 3 ? 32 : 0), wg == 3);
         tc::tmem_st_wait();
       }
+    };
+    if (nt > 0) {
+      wait_tile(0);
+      if (nt > 1) wait_tile(1);
+      widen_keys(0);
     }
     tc::fence_proxy_async();  // (the queries)
     tc::fence_before_sync();
-    if (__syncthreads_or(!ok || ctl.abort)) {
+    if (__syncthreads_or(ctl.abort)) {
       ok = false;
       break;
     }
-    if (warp == 0 && nt > 0) {
+    if (warp == kIssueS && nt > 0) {
       tc::fence_after_sync();
       issue_s(0);
     }
     if (nt > 0) ++s_count;
 
+    // a thread's rows: 8 of each half of the block, [32 h + 8 wg, 32 h + 8 wg + 8), so that a short block
+    // leaves every fourth of the warps the same share
+    const int halves = 8 * wg >= live ? 0 : kRows / 2 + 8 * wg >= live ? 1 : 2;
     for (int i = 0; i < nt; ++i) {
       const uint32_t cur = stage_of(i);
       const uint32_t buf = pv_count & 1;
-      // widen the next tile's K and this tile's V
-      if (i + 1 < nt) {
-        ok = ok && wait_tile(i + 1);
-        if (ok && k_side) {
-          widen_k<D>(stage_of(i + 1) + key * At::CW, lanes + C::K + ((i + 1) & 1) * GR * 32 + (wg == 3 ? 32 : 0), wg == 3);
-          tc::tmem_st_wait();
-        }
-      }
-      if (pv_count >= 2) ok = ok && wait_pv(pv_count - 2);  // the buffers' last readers
-      if (ok && (wg == 1 || wg == 2))
-        widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * GR * L::V_GROUP, key, wg - 1);
+      // Widen the next tile's K and this tile's V.  (That the tiles are here, and the buffers' last product
+      // done, a warp has made sure of before the last barrier.)
+      if (i + 1 < nt) widen_keys(i + 1);
+      if (wg == 1 || wg == 2) widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * GR * L::V_GROUP, key, wg - 1);
 
       // this thread's key: scales (K's with the factor that undoes the queries'), position
       const int pos = (first + i) * kTile + key;
       float sk[GR], mk[GR], sv[GR], mv[GR], smax = kSmall;
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
-        const uint32_t uk = *reinterpret_cast<const uint32_t*>(smem + (cur - sm) + At::KS + key * At::SW + 4 * gr);
-        const uint32_t uv = *reinterpret_cast<const uint32_t*>(smem + (cur - sm) + At::VS + key * At::SW + 4 * gr);
-        const bool in = pos < keys;  // (past the last key the bytes may be anything)
-        sk[gr] = in ? lo_bf16(uk) * back : 0.f;
-        mk[gr] = in ? hi_bf16(uk) * back : 0.f;
-        sv[gr] = in ? lo_bf16(uv) : 0.f;
-        mv[gr] = in ? fmaf(8.f, lo_bf16(uv), hi_bf16(uv)) : 0.f;
+        const uint32_t uk = lds32(cur + At::KS + key * At::SW + 4 * gr), uv = lds32(cur + At::VS + key * At::SW + 4 * gr);
+        sk[gr] = lo_bf16(uk) * back;
+        mk[gr] = hi_bf16(uk) * back;
+        sv[gr] = lo_bf16(uv);
+        mv[gr] = fmaf(8.f, sv[gr], hi_bf16(uv));
         smax = fmaxf(smax, sv[gr]);
       }
       const bool edge = (first + i + 1) * kTile > n0;  // some query position does not attend some key of the tile
-      ok = ok && tc::mbar_wait_warp(&ctl.s_done, (s_count - 1) & 1u, &ctl.abort, a.err);
+      if (edge && pos >= keys) {  // (past the last key the bytes may be anything)
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) sk[gr] = mk[gr] = sv[gr] = mv[gr] = 0.f;
+        smax = kSmall;
+      }
+      wait_for(&ctl.s_done, (s_count - 1) & 1u, &ctl.abort, a.err);
       tc::fence_after_sync();
 
-      const uint32_t s_at = lanes + C::S + (i & 1) * GR * kRows + wg * kShare;
+      const uint32_t s_at = lanes + C::S + (i & 1) * GR * kRows + wg * 8;
       const uint32_t p_at = sm + L::P + buf * 2 * L::P_GROUP + key * 128;
-      f32x2 p[kShare / 2];
       // Weights and the operand's rows.  Where some weight leaves fp16's range (the first tile of a unit, as
-      // no reference is set yet, and rarely after it) the references move and it is done once more.
+      // no reference is set yet, and rarely after it) the references move and it is done once more; a thread
+      // whose own weights fit has added them to its sums by then, which move with the references.
+      bool added = false;
       for (bool moved = false;;) {
         float big = 0.f;
-        if (ok) {
+        f32x2 p[kShare / 2];
 #pragma unroll
-          for (int h0 = 0; h0 < kShare; h0 += 8) {
+        for (int h = 0; h < 2; ++h) {
+          if (h < halves) {
             uint32_t s[GR][8];
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) tmem_ld_x8(s_at + gr * kRows + h0, s[gr]);
-#pragma unroll
-            for (int gr = 0; gr < GR; ++gr) tmem_ld_wait8(s[gr]);
+            for (int gr = 0; gr < GR; ++gr) tmem_ld_x8(s_at + gr * kRows + h * (kRows / 2), s[gr]);
+            const float* at = tab + h * (kRows / 2) + wg * 8;
             f32x2 x[4];
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {  // rows 2 k .. 2 k + 3
-              const int row = wg * kShare + h0 + 2 * k;
-              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(tab + 2 * kRows + row);
-              const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(tab + row);
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(at + 2 * kRows + 2 * k);
+              const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(at + 2 * k);
               x[k] = f2_fma(f2_make(mk[0], mk[0]), q0.x, m.x);
               x[k + 1] = f2_fma(f2_make(mk[0], mk[0]), q0.y, m.y);
               if constexpr (GR == 2) {
-                const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(tab + kRows + row);
+                const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(at + kRows + 2 * k);
                 x[k] = f2_fma(f2_make(mk[1], mk[1]), q1.x, x[k]);
                 x[k + 1] = f2_fma(f2_make(mk[1], mk[1]), q1.y, x[k + 1]);
               }
             }
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) tmem_ld_wait8(s[gr]);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -428,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
                 x[k] = f2_fma(f2_make(sk[gr], sk[gr]),
                               f2_make(__uint_as_float(s[gr][2 * k]), __uint_as_float(s[gr][2 * k + 1])), x[k]);
             if (edge) {
-              const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare + h0;
+              const int* lim = reinterpret_cast<const int*>(at) + 4 * kRows;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 float x0, x1;
@@ -442,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               float x0, x1;
               f2_split(x[k], x0, x1);
               const f32x2 pp = f2_make(ex2(x0), ex2(x1));
-              p[h0 / 2 + k] = pp;
+              p[4 * h + k] = pp;
               float w0, w1;
               f2_split(f2_mul(pp, f2_make(smax, smax)), w0, w1);
               big = max3f(big, w0, w1);
@@ -452,17 +474,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
                 pk[gr][k] = as_u32(__floats2half2_rn(w0, w1));
               }
             }
-            const int chunk = (wg * kShare + h0) / 8;
+            const int chunk = 4 * h + wg;
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr)
               sts128(p_at + gr * L::P_GROUP + ((chunk ^ (key & 7)) << 4), pk[gr][0], pk[gr][1], pk[gr][2], pk[gr][3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[4 * h + k] = 0;
           }
+        }
+        const bool fits = big <= kLimit;
+        if (!added && (fits || moved)) {
+          added = true;
+          if (edge && (mv[0] != mv[0] || mv[GR - 1] != mv[GR - 1])) {
+            // a row that is not finite: query positions that do not attend it must not multiply by it
+            const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * 8;
+#pragma unroll
+            for (int j = 0; j < kShare / 2; ++j) {
+              float p0, p1;
+              f2_split(p[j], p0, p1);
+              const int row = (j >> 2) * (kRows / 2) + 2 * (j & 3);
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr)
+                pm[gr][j] = f2_add(pm[gr][j], f2_make(pos < lim[row] ? p0 * mv[gr] : 0.f, pos < lim[row + 1] ? p1 * mv[gr] : 0.f));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kShare / 2; ++j)
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_fma(p[j], f2_make(mv[gr], mv[gr]), pm[gr][j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kShare / 2; ++j) l[j] = f2_add(l[j], p[j]);
+        }
+        if (warp == kThreads / 32 - 1) {  // what the next tile's start relies on
+          if (i + 2 < nt) wait_tile(i + 2);
+          if (pv_count > 0) wait_pv(pv_count - 1);
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
-        if (!__syncthreads_or((!moved && !(big <= kLimit)) || !ok || ctl.abort)) break;
-        if (ok && pv_count > pv0) ok = wait_pv(pv_count - 1);  // O is still
-        if (__syncthreads_or(!ok || ctl.abort)) {
+        if (!__syncthreads_or((!moved && !fits) || ctl.abort)) break;
+        // References move, or a wait gave up.  (O is still: its last product has been waited for.)
+        if (__syncthreads_or(ctl.abort)) {
           ok = false;
           break;
         }
@@ -471,15 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         // every row's largest logit + log2 of the key's scale, first over the warps
         const float ls = __log2f(smax);
 #pragma unroll 1
-        for (int r = 0; r < kShare; r += 4) {
+        for (int r = 0; r < 8 * halves; r += 4) {
+          const int row0 = (r >> 3) * (kRows / 2) + wg * 8 + (r & 4);
           uint32_t s[GR][4];
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_x4(s_at + gr * kRows + r, s[gr]);
+          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_x4(s_at - wg * 8 + gr * kRows + row0, s[gr]);
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_wait4(s[gr]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = wg * kShare + r + k;
+            const int row = row0 + k;
             float x = 0.f;
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), fmaf(mk[gr], tab[gr * kRows + row], x));
@@ -489,22 +543,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         __syncthreads();
         if (tid < kRows) {
-          const float z = fmaxf(fmaxf(red[tid], red[kRows + tid]), fmaxf(red[2 * kRows + tid], red[3 * kRows + tid]));
-          const float m0 = -tab[2 * kRows + tid];
           float f = 1.f;
-          if (z - m0 > 14.9f) {
-            f = ex2(m0 - (z - kHeadroom));
-            tab[2 * kRows + tid] = kHeadroom - z;
+          if ((tid & ~7) < live) {  // (rows behind the last share its eight)
+            const float z = fmaxf(fmaxf(red[tid], red[kRows + tid]), fmaxf(red[2 * kRows + tid], red[3 * kRows + tid]));
+            const float m0 = -tab[2 * kRows + tid];
+            if (z - m0 > 14.9f) {
+              f = ex2(m0 - (z - kHeadroom));
+              tab[2 * kRows + tid] = kHeadroom - z;
+            }
           }
           tab[3 * kRows + tid] = f;
         }
         __syncthreads();
-        const f32x2* f = reinterpret_cast<const f32x2*>(tab + 3 * kRows + wg * kShare);
+        const f32x2* f = reinterpret_cast<const f32x2*>(tab + 3 * kRows + wg * 8);
 #pragma unroll
         for (int j = 0; j < kShare / 2; ++j) {
-          l[j] = f2_mul(l[j], f[j]);
+          const f32x2 fj = f[(j >> 2) * (kRows / 4) + (j & 3)];
+          l[j] = f2_mul(l[j], fj);
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_mul(pm[gr][j], f[j]);
+          for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_mul(pm[gr][j], fj);
         }
         if (pv_count > pv0) {
           // this thread's row (lane) of O, a quarter of its group's channels
@@ -522,29 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
       }
       if (!ok) break;
-      if (edge && (mv[0] != mv[0] || mv[GR - 1] != mv[GR - 1])) {
-        // a row that is not finite: query positions that do not attend it must not multiply by it
-        const int* lim = reinterpret_cast<const int*>(tab) + 4 * kRows + wg * kShare;
-#pragma unroll
-        for (int j = 0; j < kShare / 2; ++j) {
-          float p0, p1;
-          f2_split(p[j], p0, p1);
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-            pm[gr][j] = f2_add(pm[gr][j], f2_make(pos < lim[2 * j] ? p0 * mv[gr] : 0.f,
-                                                  pos < lim[2 * j + 1] ? p1 * mv[gr] : 0.f));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kShare / 2; ++j)
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr) pm[gr][j] = f2_fma(p[j], f2_make(mv[gr], mv[gr]), pm[gr][j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kShare / 2; ++j) l[j] = f2_add(l[j], p[j]);
-      if (warp == 0) {
+      if (warp == kIssueS) {
         tc::fence_after_sync();
         if (i + 1 < nt) issue_s(i + 1);
+      } else if (warp == kIssuePV) {
+        tc::fence_after_sync();
         issue_pv(i, pv_count);
       } else if (tid == kFetcher) {
         fetch_tile<D, kStages>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);  // into this tile's stage
@@ -557,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
 
     // Sums over the keys: the two half-warps, then 16 rows over 16 lanes (each step halves the rows a lane
     // holds), then the warps.
-    if (nt > 0) ok = wait_pv(pv_count - 1);
+    if (nt > 0) wait_pv(pv_count - 1);
     tc::fence_after_sync();
     auto scatter = [&](const f32x2 (&pairs)[kShare / 2]) {
       float v[kShare];
@@ -582,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       return v[0];
     };
     {
-      float* mine = red + (qd * kRows + wg * kShare + (lane & 15)) * 3;
+      float* mine = red + (qd * kRows + (lane & 8) * (kRows / 16) + wg * 8 + (lane & 7)) * 3;
       const float sl = scatter(l);
       if (lane < 16) mine[0] = sl;
 #pragma unroll
@@ -591,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         if (lane < 16) mine[1 + gr] = sp;
       }
     }
-    if (__syncthreads_or(!ok || ctl.abort)) {
+    if (__syncthreads_or(ctl.abort)) {
       ok = false;
       break;
     }
