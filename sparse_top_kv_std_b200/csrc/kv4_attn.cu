@@ -11,7 +11,9 @@
 // fp32 sum; powers of two in q and in the result undo it.  One mask for two codes is all that widening
 // costs.  (The sum over keys has to be centred, b - 8, because sum p b grows without bound while the
 // answer stays near the mean: at 140,000 keys the fp32 accumulator would lose it.  A product with a
-// matrix of eights, one for sixteen, gathers 8 sum p sv, and is subtracted every few tiles.)
+// matrix of eights, one for sixteen, gathers 8 sum p sv, and is subtracted every few tiles.  What the
+// accumulator's own rounding loses until then is 1e-4 of a bf16 result's last place but 5e-5 of the
+// result over 2,000 keys: for fp32 queries all codes are centred before they are multiplied.)
 //
 // A byte of the cache feeds 2 G x rows multiply-adds, and a key's codes have to be widened
 // before any of them: at d = 128 a (row, head) is 144 bytes, against 512 in bf16, and its 256
@@ -94,6 +96,13 @@ __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<
 // Two codes as fp16 subnormals: c 2^-24 from bits 0-3 and 16-19, c 2^-20 from bits 4-7 and 20-23.
 __device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
 __device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
+// Two codes as c - 8, one instruction more: 0x6400 is 1024, whose last ten bits hold a code at bit 0 or 4.
+__device__ __forceinline__ uint32_t centre0(uint32_t w) {
+  return as_u32(__hsub2(as_h2(widen0(w) | 0x64006400u), __float2half2_rn(1032.f)));
+}
+__device__ __forceinline__ uint32_t centre4(uint32_t w) {
+  return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
+}
 constexpr uint32_t kEight0 = 0x00080008u, kEight4 = 0x00800080u;  // the code 8 in either place
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -157,8 +166,9 @@ struct State {
   float back;                                // K's scales times this: undoes q's scaling, log2(e) / sqrt(d)
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
-  float o[NT][MT][4];                        // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8)
-  float eight[NT][GR][4];                    // sum (p sv) 8 of the same keys since the last settle(), same units
+  // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8); fp32 queries: sum (p sv) (b - 8)
+  float o[NT][MT][4];
+  float eight[F32 ? 1 : NT][GR][4];          // sum (p sv) 8 of the same keys since the last settle(), same units
 };
 
 template <int D, int NT, bool F32>
@@ -203,9 +213,9 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
   int ex = (int)(__float_as_uint(top) >> 23) - 127;
   ex = ex < -100 ? -100 : ex;
   const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-  // the products come out in units of 2^(ex - 14) 2^24
-  st.back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)((ex > 100 ? ex - 10 : ex + 10) + 127) << 23);
-  if (ex > 100) st.back *= 1048576.f;
+  // the products come out in units of 2^(ex - 14), and 2^24 where the codes are subnormals
+  st.back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+  if constexpr (!F32) st.back *= 16777216.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float sum[S::GR];
@@ -223,7 +233,7 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // channels i and i + 4 of the word: one register; odd i meet codes at 2^-20
-          const float x0 = y[i] * (i & 1 ? 0.0625f : 1.f), x1 = y[i + 4] * (i & 1 ? 0.0625f : 1.f);
+          const float x0 = y[i] * (i & 1 && !F32 ? 0.0625f : 1.f), x1 = y[i + 4] * (i & 1 && !F32 ? 0.0625f : 1.f);
           const __half2 hv = __floats2half2_rn(x0, x1);
           const float2 f = __half22float2(hv);
           hi[i] = as_u32(hv);
@@ -235,7 +245,7 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       }
     }
 #pragma unroll
-    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]) * 5.9604645e-8f;  // 2^-24
+    for (int gr = 0; gr < S::GR; ++gr) sum[gr] = quad_sum(sum[gr]) * (F32 ? 1.f : 5.9604645e-8f);  // 2^-24
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int from = 4 * (2 * t + e);  // a lane that holds row 2 t + e
@@ -251,7 +261,7 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
 #pragma unroll
       for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] = 0.f;
 #pragma unroll
-      for (int gr = 0; gr < S::GR; ++gr) st.eight[nt][gr][i] = 0.f;
+      for (int gr = 0; gr < S::GR; ++gr) st.eight[F32 ? 0 : nt][gr][i] = 0.f;
     }
   }
 }
@@ -260,14 +270,15 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
 template <int D, int NT, bool F32>
 __device__ __forceinline__ void settle(State<D, NT, F32>& st) {
   using S = State<D, NT, F32>;
+  if constexpr (F32) return;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] -= st.eight[nt][mt / 4][i];
+      for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] -= st.eight[F32 ? 0 : nt][mt / 4][i];
 #pragma unroll
-      for (int gr = 0; gr < S::GR; ++gr) st.eight[nt][gr][i] = 0.f;
+      for (int gr = 0; gr < S::GR; ++gr) st.eight[F32 ? 0 : nt][gr][i] = 0.f;
     }
 }
 
@@ -313,7 +324,7 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
   // The 16 keys' scales to fp32, one half-warp for K and one for V, (s, m) of both groups: each lane
   // needs two keys' of each, and four lanes the same ones.
   {
-    const float c = lane < 16 ? 0.f : 8.f, f = lane < 16 ? st.back : 1.f;
+    const float c = lane < 16 && !F32 ? 0.f : 8.f, f = lane < 16 ? st.back : 1.f;
     if constexpr (GR == 2) {
       const uint2 u = lds64(at.scale + tile);
       const float s0 = lo_bf16(u.x), s1 = lo_bf16(u.y);
@@ -352,7 +363,8 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t x = k ? wa[w] >> 8 : wa[w], y = k ? wb[w] >> 8 : wb[w];
-      const uint32_t a0 = widen0(x), a1 = widen0(y), a2 = widen4(x), a3 = widen4(y);
+      const uint32_t a0 = F32 ? centre0(x) : widen0(x), a1 = F32 ? centre0(y) : widen0(y);
+      const uint32_t a2 = F32 ? centre4(x) : widen4(x), a3 = F32 ? centre4(y) : widen4(y);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float(&c)[4] = acc[nt][gr];
@@ -444,8 +456,10 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr) {
             st.pm[nt][gr][e] *= f;
-            st.eight[nt][gr][e] *= f;
-            st.eight[nt][gr][2 + e] *= f;
+            if constexpr (!F32) {
+              st.eight[nt][gr][e] *= f;
+              st.eight[nt][gr][2 + e] *= f;
+            }
           }
 #pragma unroll
           for (int mt = 0; mt < S::MT; ++mt) {
@@ -478,10 +492,10 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
           pl[nt][gr][hf] = transpose8x8(as_u32(__floats2half2_rn(w0 - f.x, w1 - f.y)));
         }
       }
+    if constexpr (!F32) {
 #pragma unroll
-    for (int gr = 0; gr < GR; ++gr) {
-      mma_f16(st.eight[nt][gr], kEight0, kEight4, kEight0, kEight4, ph[nt][gr][0], ph[nt][gr][1]);
-      if constexpr (F32) mma_f16(st.eight[nt][gr], kEight0, kEight4, kEight0, kEight4, pl[nt][gr][0], pl[nt][gr][1]);
+      for (int gr = 0; gr < GR; ++gr)
+        mma_f16(st.eight[nt][gr], kEight0, kEight4, kEight0, kEight4, ph[nt][gr][0], ph[nt][gr][1]);
     }
   }
 
@@ -511,7 +525,8 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t b01 = k ? y01 >> 8 : y01, b23 = k ? y23 >> 8 : y23;
-        const uint32_t a0 = widen0(b01), a1 = widen4(b01), a2 = widen0(b23), a3 = widen4(b23);
+        const uint32_t a0 = F32 ? centre0(b01) : widen0(b01), a1 = F32 ? centre4(b01) : widen4(b01);
+        const uint32_t a2 = F32 ? centre0(b23) : widen0(b23), a3 = F32 ? centre4(b23) : widen4(b23);
         const int mt = gr * 4 + hw * 2 + k;  // rows g: channel 8 g + 2 (2 hw + k), rows g + 8: the next one
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -544,8 +559,8 @@ __device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4Attn
         const float c = column_sum(st.pm[nt][gr][e]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          st.o[nt][gr * 4 + i][e] = fmaf(st.o[nt][gr * 4 + i][e], 16777216.f, c);         // 2^24
-          st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], 1048576.f, c);  // 2^20
+          st.o[nt][gr * 4 + i][e] = fmaf(st.o[nt][gr * 4 + i][e], F32 ? 1.f : 16777216.f, c);         // 2^24
+          st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], F32 ? 1.f : 1048576.f, c);  // 2^20
         }
       }
       const int n = nt * 8 + 2 * t + e;

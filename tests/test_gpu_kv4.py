@@ -301,6 +301,20 @@ def test_moving_references_and_scales(dtype, kind, scale, Hq, rows):
     _check(o, q, c, lens, 1, dtype)
 
 
+@pytest.mark.parametrize("n", [700, 2112, 30000])
+@pytest.mark.parametrize("d,Hq,rows", [(64, 2, 1), (128, 1, 1), (128, 5, 3)])
+def test_fp32_results_keep_fp32_accuracy(n, d, Hq, rows):
+    """Diffuse attention, where the result is a small difference of large sums.  A fp32 accumulator of a
+    tensor core is off by at most 2^-23 of its size a step; over a warp's n / 128 or fewer steps of
+    centred codes, whose sums grow like sqrt(n), that is below sqrt(n / 128) 2^-23 of the result, 2e-6
+    here; the logits' own rounding (2^-22 of some 30 in each) adds as much, at random."""
+    dims, q, c, cv, _ = _attn_inputs(1, 1, Hq, 1, d, rows, [n], 0, torch.float32, seed=n)
+    o = _attend(dims, q, rows, c, cv, [n], 0)
+    want, _ = _want(q, c, [n], 0, torch.float32)
+    err = np.linalg.norm(o.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= 8e-6, err
+
+
 @pytest.mark.parametrize("dtype,Hq,rows", [(torch.bfloat16, 7, 1), (torch.float32, 2, 1), (torch.bfloat16, 7, 7)])
 def test_long_context_split_over_the_device(dtype, Hq, rows):
     lens = [70001, 33333]
