@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Args a, int
   for (int u = 0; u < kUnroll; ++u) {
     const int r = r0 + u * RPB;
     word[u] = sc[u] = 0;
-    if (r < sp.n) {
+    if (r < sp.n && STD_DCHECK(sp.pos + r < a.cap, a.err)) {
       const int64_t row = (int64_t)prob * a.cap + sp.pos + r;
       word[u] = __ldcs(codes + row * LPR + w);
       sc[u] = __ldg(scales + row * (D / kKv4Group) + grp);
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Args a, int
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int r = r0 + u * RPB;
-    if (r >= sp.n) break;
+    if (r >= sp.n || !STD_DCHECK(r < a.rows_cap, a.err)) break;
     const float s = __uint_as_float(sc[u] << 16), m = __uint_as_float(sc[u] & 0xffff0000u);
     // 2^23 + c, one byte permutation, less 2^23
     const uint32_t even = word[u] & 0x0f0f0f0fu, odd = (word[u] >> 4) & 0x0f0f0f0fu;

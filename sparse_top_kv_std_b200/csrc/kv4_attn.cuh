@@ -153,11 +153,15 @@ __device__ __forceinline__ void fetch_tile(const Kv4AttnArgs& a, Fetch* f, const
   const int64_t row = f->row0 + first;
   const uint32_t dst = ring + stage * At::BYTES;
   uint64_t* bar = &full[stage];
-  tc::mbar_expect_tx(bar, 2 * rows * (At::CW + At::SW));
-  bulk_load(dst, a.k_codes + row * At::CW, rows * At::CW, bar);
-  bulk_load(dst + At::KS, a.k_scales + row * At::SW, rows * At::SW, bar);
-  bulk_load(dst + At::VC, a.v_codes + row * At::CW, rows * At::CW, bar);
-  bulk_load(dst + At::VS, a.v_scales + row * At::SW, rows * At::SW, bar);
+  if (STD_DCHECK(first >= 0 && first + (int64_t)rows <= a.cap && row >= 0, a.err)) {
+    tc::mbar_expect_tx(bar, 2 * rows * (At::CW + At::SW));
+    bulk_load(dst, a.k_codes + row * At::CW, rows * At::CW, bar);
+    bulk_load(dst + At::KS, a.k_scales + row * At::SW, rows * At::SW, bar);
+    bulk_load(dst + At::VC, a.v_codes + row * At::CW, rows * At::CW, bar);
+    bulk_load(dst + At::VS, a.v_scales + row * At::SW, rows * At::SW, bar);
+  } else {
+    tc::mbar_arrive(bar);  // (debug build: the tile is left as it is)
+  }
   f->fills += 1;
   f->first = first + kTile;
   f->left -= 1;

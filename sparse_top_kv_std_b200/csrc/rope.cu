@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) q
     return;
   }
   if (r0 >= n) return;
+  if ((a.k_in || a.v_in) && !STD_DCHECK(base >= 0 && base + n <= a.cap, a.err)) return;
   const int ntok = n - r0 < TOK ? n - r0 : TOK;
 
   // this half-warp's token and share of the heads, in the order q, k, v
