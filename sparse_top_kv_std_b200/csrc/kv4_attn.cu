@@ -149,6 +149,12 @@ __device__ __forceinline__ float column_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
 
+__device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {  // (a predicate, not a branch)
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n"
+               ::"r"(bar), "r"((uint32_t)on)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- a warp's state for one unit
 // Lane = 4 g + t.  Query rows are the n index of the matrix instructions: as an operand a lane
 // holds row g of each 8-row block, in an accumulator rows 2 t and 2 t + 1.  Accumulator row
@@ -639,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     for (int s = 0; s < STAGES; ++s) fetch_tile<D, STAGES>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
   }
   const LaneAt<D, NT, F32> at(warp, lane);
+  const uint32_t full_at = smem_u32(ctl.full), empty_at = smem_u32(ctl.empty);
   int stage = 0, turn = -1;  // turn: tiles read before this one, mod kWarps (-1: none)
   uint32_t phase = 0;
   for (int t = begin; t < end;) {
@@ -656,7 +663,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
     __syncthreads();
     key0 += 16 * warp;
     for (; left > 0; --left, key0 += kTile) {
-      if (!tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err)) break;
+      if (!__all_sync(0xffffffffu, tc::mbar_try_wait(full_at + 8 * stage, phase)) &&
+          !tc::mbar_wait_warp(&ctl.full[stage], phase, &ctl.abort, a.err))
+        break;
       const uint32_t tile = ring + stage * Lay::STAGE;
       if (key0 + 16 <= n0) {
         attend16<D, NT, F32, false>(st, at, ring, tile, 0, 0, 0, 1, 0, lane);
@@ -667,21 +676,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? 2 : 1) kv4_attn_ke
       // have most likely left by now.  A fetch comes before its warp leaves this tile, so fetches
       // happen one at a time and in order.
       __syncwarp();
-      if (lane == 0) {
-        if (turn == warp) {
+      if (turn == warp) {
+        if (lane == 0) {
           const int before = stage == 0 ? STAGES - 1 : stage - 1;
           if (tc::mbar_wait(&ctl.empty[before], stage == 0 ? phase ^ 1 : phase, &ctl.abort, a.err))
             fetch_tile<D, STAGES>(a, &ctl.fetch, ctl.split, ctl.full, ring, end);
         }
-        tc::mbar_arrive(&ctl.empty[stage]);
+        __syncwarp();
       }
-      __syncwarp();
+      arrive_if(lane == 0, empty_at + 8 * stage);
       turn = (turn + 1) & (kWarps - 1);
       if (turn == 0) settle(st);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
+      const bool wrap = stage == STAGES - 1;
+      phase ^= wrap;
+      stage = wrap ? 0 : stage + 1;
     }
     const Unit u = locate(a, ctl.split, t);
     const int n = min(u.groups - u.first, end - t);
