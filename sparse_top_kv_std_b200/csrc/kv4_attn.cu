@@ -16,9 +16,10 @@
 // result over 2,000 keys: for fp32 queries all codes are centred before they are multiplied.)
 //
 // A byte of the cache feeds 2 G x rows multiply-adds, and a key's codes have to be widened
-// before any of them: at d = 128 a (row, head) is 144 bytes, against 512 in bf16, with 256 codes, and
-// at full HBM rate an SM has some 1,600 issue slots for 16 keys.  So the widened codes go straight from registers into mma.sync (m16n8k16: 16 keys or 16
-// channels by 8 query rows), with no shared-memory round trip: K is the A operand of S^T = K q^T,
+// before any of them: at d = 128 a (row, head) is 144 bytes, against 512 in bf16, with 256
+// codes, and at full HBM rate an SM has some 400 issue slots for 16 keys, three for a code and lane.  So
+// the widened codes go straight from registers into mma.sync (m16n8k16: 16 keys or 16 channels by 8
+// query rows), with no shared-memory round trip: K is the A operand of S^T = K q^T,
 // V^T the A operand of O^T = V^T P^T, and one movmatrix turns S^T's accumulator layout into
 // P^T's operand layout.  A 5th-generation MMA would need the operand written to shared or
 // tensor memory first, for 8 of its 128 columns.
@@ -28,9 +29,9 @@
 // with a softmax state of its own.  The states merge once for each unit a CTA touches; units that several
 // CTAs touch merge in a second kernel.
 //
-// Measured: 28 layers x 4 heads x 143,616 keys, 7 rows, 460 us, 5.0 TB/s of 6.46.  16 keys are some 300
-// instructions of a warp, 98 of them masks, shifts and byte permutations on a pipe of half rate; with the 16
-// warps that 126 registers leave an SM they take 530 clocks of each scheduler (the memory: 400).
+// Measured: 28 layers x 4 heads x 143,616 keys, 7 rows, 460 us, 5.0 TB/s of 6.46.  16 keys are
+// 305 instructions of a warp; with the 16 warps that 126 registers leave an SM, 57% of the issue slots and 53%
+// of the integer pipe are used: four warps a scheduler do not hide their own latencies.
 #include "kv4_attn.cuh"
 
 #include <cuda_fp16.h>
@@ -732,7 +733,9 @@ cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 // More than 16 query rows share a widened code often enough for the tensor-memory kernel (bf16; fp32
-// queries need their second fp16 term, and two weights for one, and stay here).
+// queries need their second fp16 term, and two weights for one, and stay here).  28 layers x 4 heads x
+// 33,024 keys, there / here: 16 rows 322 / 192 us, 18 rows 330 / 370, 28 rows 369 / 372, 49 rows 402 / 728.
+// (One layer of 16,512 keys: 18 rows 18.8 / 17.8, 28 rows 19.6 / 18.7, 49 rows 22.5 / 24.7.)
 static bool on_tensor_memory(const Kv4AttnArgs& a) { return a.dtype == STD_BF16 && a.rows > 16; }
 
 // Query rows of a block, and CTAs of an SM, by the kernel the call takes.

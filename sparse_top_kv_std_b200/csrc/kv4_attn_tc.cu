@@ -12,10 +12,10 @@
 // reference of each row that moves only when some weight would leave fp16's range, so a tile has one
 // barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
 //
-// A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Its products are 820 clocks of the tensor
-// cores and 640 of shared-memory bandwidth, its 8,192 weights 512 of the exponential unit, and with the
-// widened rows, the weights and the tables shared memory is busy some 1,900 clocks.  Measured: 28 layers x 4
-// heads x 33,024 keys, 49 rows, 403 us, 3,100 clocks a tile (four blocks of 16 rows in kv4_attn.cu: 723 us).
+// A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
+// x 4 heads x 33,024 keys, 49 rows, 403 us (four blocks of 16 rows in kv4_attn.cu: 728 us), 3,700 clocks a
+// tile.  In them the tensor cores are busy 800, the warps' shared-memory traffic (widened rows, weights,
+// tables) takes 1,940 and the issue slots are 55% used: what bounds a tile is that its phases follow each other.
 #include "kv4_attn.cuh"
 
 #include <cuda_fp16.h>
