@@ -870,8 +870,9 @@ int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_i
   }
   if (sum != rope->rot_dim / 2)
     return fail(STD_ERR_INVALID_ARG, "the sections hold %d pairs, rot_dim / 2 = %d", sum, rope->rot_dim / 2);
-  // (the kernel numbers its CTAs in 31 bits: one for a few tokens of a sequence at least)
-  if ((int64_t)dims->L * dims->B * (rows / 4 + 1) > (1 << 30)) return fail(STD_ERR_INVALID_ARG, "too many tokens");
+  // (the kernel numbers tokens in 31 bits, those that a last CTA would have past the end too)
+  if ((int64_t)dims->L * dims->B > INT32_MAX || (int64_t)dims->L * dims->B * rows > INT32_MAX - 1024)
+    return fail(STD_ERR_INVALID_ARG, "too many tokens");
   int *err, sms;
   STD_TRY(device_state(&err, &sms));
   stdb::RopeArgs a{};
@@ -915,7 +916,9 @@ int run_kv4(const std_dims* dims, const std_kv4_cache* c, const void* k, const v
   // with counts on the device max_n is a bound, which may pass the capacity
   if (!count && (int64_t)max_n + pos_offset > c->cap) return fail(STD_ERR_CAPACITY, "offset + rows exceed cap");
   if (!count && at_pos && max_n > rows_cap) return fail(STD_ERR_CAPACITY, "rows exceed cap_full");
-  if (2 * (int64_t)probs_of(dims) * (max_n / 64 + 1) > INT32_MAX) return fail(STD_ERR_INVALID_ARG, "too many rows");
+  // (the kernels number CTAs and a sequence's rows in 31 bits, those that a last CTA would have past the end too)
+  if (max_n > INT32_MAX - 1024 || 2 * (int64_t)probs_of(dims) * (max_n / 64 + 1) > INT32_MAX)
+    return fail(STD_ERR_INVALID_ARG, "too many rows");
   int* err;
   STD_TRY(device_state(&err, nullptr));
   stdb::Kv4Args a{};

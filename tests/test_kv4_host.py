@@ -197,3 +197,14 @@ def test_binding_refuses_uneven_token_views():
             B._tokens(view, 1, 2, 4, 64, -1)
     with pytest.raises(ValueError):
         B.std_rope(torch.zeros(32), sections=[32])               # not float64
+
+
+@no_gpu_only
+def test_row_counts_that_pass_31_bits_are_refused():
+    one = dict(dims=_dims(L=1, B=1, Hq=4, Hkv=1), k=None, v=None, pos=FAKE)
+    for n in (2**31 - 1, 2**31 - 100):
+        assert _call_rope(rows=n, **one) == _INV
+        for begin in (None, FAKE):
+            assert _lib().std_kv4_quantize(_dims(L=1, Hkv=1, Hq=4), _cache(), FAKE, FAKE, begin, FAKE, n, None) == _INV
+            assert _lib().std_kv4_read(_dims(L=1, Hkv=1, Hq=4), _cache(), begin, FAKE, n, FAKE, FAKE, None) == _INV
+    assert _call_rope(rows=2**28, dims=_dims(L=4, B=4, Hq=4, Hkv=1), k=None, v=None, pos=FAKE) == _INV
