@@ -401,6 +401,7 @@ def std_rope(inv_freq, sections=None, interleaved=False) -> StdRope:
     r = StdRope(_ptr(inv_freq), 2 * half, int(interleaved), len(sections),
                 (ctypes.c_int32 * 3)(*(sections + [0] * (3 - len(sections)))))
     r.keep = inv_freq
+    r.device = None if inv_freq is None else inv_freq.get_device()
     return r
 
 
@@ -417,9 +418,9 @@ _device = None
 
 
 def _on(x, dev) -> Optional[int]:
-    """Pointer of a contiguous tensor on device `dev`, the one the call runs on."""
-    if x is None:
-        return None
+    """Pointer of a contiguous tensor on device `dev`, the one the call runs on (or an address)."""
+    if x is None or isinstance(x, int):
+        return x
     if x.get_device() != dev:
         raise ValueError("expected a CUDA tensor on the current device")
     if not x.is_contiguous():
@@ -439,6 +440,8 @@ def _tokens(x, L, nB, heads, d, dev):
         raise ValueError(f"expected [{L}][{nB}][rows][{heads}][{d}], got {tuple(shape)}")
     s0, s1, s, s3, s4 = x.stride()
     rows = shape[2]
+    if rows == 0:
+        return None, heads * d
     if rows == 1:
         s = s1 if nB > 1 else s0 if L > 1 else heads * d
     if s4 != 1 or (heads > 1 and s3 != d) or (nB > 1 and s1 != rows * s) or (L > 1 and s0 != nB * rows * s):
@@ -454,6 +457,11 @@ def std_qk_norm_rope(d: StdDims, rope: StdRope, q_in, k_in, v_in, rows, n_rows, 
     q, qs = _tokens(q_in, L, nB, d.Hq, hd, dev)
     k, ks = _tokens(k_in, L, nB, Hkv, hd, dev)
     v, vs = _tokens(v_in, L, nB, Hkv, hd, dev)
+    for x in (q_in, k_in, v_in):
+        if x is not None and x.shape[2] != rows:
+            raise ValueError(f"expected {rows} rows, got {x.shape[2]}")
+    if getattr(rope, "device", None) not in (None, dev):
+        raise ValueError("expected inv_freq on the current device")
     _check(lib().std_qk_norm_rope(ctypes.byref(d), ctypes.byref(rope), q, qs, k, ks, v, vs, rows, _on(n_rows, dev),
                                   _on(q_weight, dev), _on(k_weight, dev), eps, _on(pos, dev), _on(q_out, dev),
                                   _on(k_cache, dev), _on(v_cache, dev), cap, _on(length, dev), pos_offset,

@@ -208,3 +208,30 @@ def test_row_counts_that_pass_31_bits_are_refused():
             assert _lib().std_kv4_quantize(_dims(L=1, Hkv=1, Hq=4), _cache(), FAKE, FAKE, begin, FAKE, n, None) == _INV
             assert _lib().std_kv4_read(_dims(L=1, Hkv=1, Hq=4), _cache(), begin, FAKE, n, FAKE, FAKE, None) == _INV
     assert _call_rope(rows=2**28, dims=_dims(L=4, B=4, Hq=4, Hkv=1), k=None, v=None, pos=FAKE) == _INV
+
+
+def test_binding_checks_rows_devices_and_takes_addresses(monkeypatch):
+    torch = pytest.importorskip("torch")
+    calls = []
+    fake = type("Lib", (), {"std_qk_norm_rope": lambda self, *a: calls.append(a) or 0})()
+    monkeypatch.setattr(B, "lib", lambda: fake)
+    monkeypatch.setattr(B, "_current_device", lambda: -1)        # what a CPU tensor's get_device() gives
+    monkeypatch.setattr(B, "_stream", lambda s: None)
+    monkeypatch.setattr(B, "_ptr", lambda x: None if x is None else x.data_ptr())
+    d, out = B.dims(1, 2, 4, 2, 64, B.STD_F32, 8, 1), torch.zeros(1)
+
+    def call(q, rows, rope, pos=None):
+        B.std_qk_norm_rope(d, rope, q, None, None, rows, None, None, None, 1e-6, pos, out, None, None, 8, None)
+
+    rope = B.std_rope(torch.zeros(32, dtype=torch.float64))
+    call(torch.zeros(1, 2, 3, 4, 64), 3, rope)
+    for rows in (2, 4):                                          # not the rows that the tensor has
+        with pytest.raises(ValueError):
+            call(torch.zeros(1, 2, 3, 4, 64), rows, rope)
+    call(torch.zeros(1, 2, 0, 4, 64), 0, rope)                   # no rows of several sequences
+    call(torch.zeros(1, 2, 3, 4, 64), 3, rope, pos=4096)         # an address, as in the other calls
+    assert len(calls) == 3 and calls[2][13] == 4096
+    other = B.std_rope(torch.zeros(32, dtype=torch.float64))
+    other.device = 1                                             # frequencies on another GPU
+    with pytest.raises(ValueError):
+        call(torch.zeros(1, 2, 3, 4, 64), 3, other)
