@@ -78,6 +78,7 @@ __device__ __forceinline__ void pack(const float (&x)[E], Vec<E * sizeof(T)>& v)
   }
 }
 
+constexpr int64_t kNoToken = INT64_MIN;
 constexpr int kBatch = 4;  // heads a half-warp has in flight
 
 // What a half-warp does of one part (q, k or v) of its token: n heads, from src / dst on, a head apart
@@ -172,57 +173,66 @@ __device__ __forceinline__ void run_heads(Vec<E * sizeof(T)> (&v)[kBatch], const
   }
 }
 
-// One CTA: TOK neighbouring tokens of one (layer, sequence), 16 / TOK half-warps on each, and one of
+// One CTA: TOK neighbouring tokens of one (layer, sequence), or (SHARED) of all of them, 16 / TOK half-warps
+// on each; `count` is the chunks of TOK tokens of a sequence, or all tokens.  It takes one of
 // `head_parts` equal shares of their heads.  E = d / 16 channels a lane.  A lane keeps its cosines and
 // sines for all heads of its token and has kBatch heads' loads in flight, the first ones before the
 // angles are formed.  33,024 tokens of 28 + 4 + 4 heads, d = 128, bf16: 124 us, 4.9 TB/s of 6.46; eight
 // tokens a CTA took 205 us with cosines and sines read from shared memory for each head, 173 with a
 // shuffle for each normalised channel, 148 as it is.
-template <typename T, int E, int TOK>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) qk_norm_rope_kernel(const RopeArgs a, int chunks, int head_parts) {
+template <typename T, int E, int TOK, bool SHARED>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) qk_norm_rope_kernel(const RopeArgs a, int count, int head_parts) {
   __shared__ float2 cs[TOK][8 * E];
+  __shared__ int64_t at[SHARED ? TOK : 1];
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
   constexpr int D = 16 * E, HS = kHeadsAtOnce / TOK;
-  const int part = blockIdx.x % head_parts;
-  const int rest = blockIdx.x / head_parts;
-  const int lb = rest / chunks, b = lb % a.B, l = lb / a.B;
-  const int r0 = (rest % chunks) * TOK;
-  const int n = a.n_rows ? a.n_rows[b] : a.rows;
-  const int64_t base = (a.len ? (int64_t)a.len[b] : 0) + a.pos_offset;
-  if (n < 0 || n > a.rows) {
-    if (r0 == 0 && part == 0 && threadIdx.x == 0) flag_error(a.err, STD_DEVERR_LENGTH);
-    return;
-  }
-  if ((a.k_in || a.v_in) && (base < 0 || base + n > a.cap)) {
-    if (r0 == 0 && part == 0 && threadIdx.x == 0) flag_error(a.err, STD_DEVERR_CAPACITY);
-    return;
-  }
-  if (r0 >= n) return;
-  if ((a.k_in || a.v_in) && !STD_DCHECK(base >= 0 && base + n <= a.cap, a.err)) return;
-  const int ntok = n - r0 < TOK ? n - r0 : TOK;
-
-  // this half-warp's token and share of the heads, in the order q, k, v
-  const int hw = threadIdx.x >> 4, t = min(hw / HS, ntok - 1);
-  const int e0 = (threadIdx.x & 15) * E;
+  const int part = blockIdx.x % head_parts, rest = blockIdx.x / head_parts;
+  const int hw = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * E;
   const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+  // this half-warp's token: row r of sequence b in layer l, cache row base + r
+  const int t = hw / HS;
+  const int tok = rest * TOK + t;  // (SHARED)
+  const int lb = SHARED ? (tok < count ? tok / a.rows : 0) : rest / count;
+  const int r = SHARED ? tok - lb * a.rows : (rest - lb * count) * TOK + t;
+  const int l = lb / a.B, b = lb - l * a.B;
+  bool ok = !SHARED || tok < count;
+  int64_t base = 0;
+  int n = 0;
+  if (ok) {
+    n = a.n_rows ? a.n_rows[b] : a.rows;
+    base = (a.len ? (int64_t)a.len[b] : 0) + a.pos_offset;
+    const bool counted = n >= 0 && n <= a.rows;
+    const bool fits = !(a.k_in || a.v_in) || (base >= 0 && base + n <= a.cap);
+    if (!(counted && fits) && r == 0 && part == 0 && (threadIdx.x & 15) == 0)
+      flag_error(a.err, counted ? STD_DEVERR_CAPACITY : STD_DEVERR_LENGTH);
+    ok = counted && fits && r < n;
+    if (!SHARED && !(counted && fits && r - t < n)) return;  // (the same for the CTA: none of its tokens)
+    if (ok && (a.k_in || a.v_in)) ok = STD_DCHECK(base >= 0 && base + r < a.cap, a.err);
+  }
+  // its place in `pos`, or its position
+  if constexpr (SHARED) {
+    if ((threadIdx.x & 15) == 0 && hw % HS == 0) at[t] = !ok ? kNoToken : a.pos ? (int64_t)b * a.rows + r : base + r;
+  }
+
+  // its share of the heads, in the order q, k, v
   const int nq = a.q_in ? a.Hq : 0, nk = a.k_in ? a.Hkv : 0, nv = a.v_in ? a.Hkv : 0;
   const int heads = nq + nk + nv, shares = HS * head_parts, share = part * HS + hw % HS;
   const int h0 = (int)((int64_t)heads * share / shares);
-  const int h1 = hw / HS < ntok ? (int)((int64_t)heads * (share + 1) / shares) : h0;
+  const int h1 = ok ? (int)((int64_t)heads * (share + 1) / shares) : h0;
   auto part_of = [&](int which) {  // 0, 1, 2: q, k, v
-    const int64_t tok = (int64_t)lb * a.rows + r0 + t;
+    const int64_t tok = (int64_t)lb * a.rows + r;
     Part<T> p;
     if (which == 0) {
       p.src = static_cast<const T*>(a.q_in) + tok * a.q_stride + h0 * D;
-      p.dst = static_cast<T*>(a.q_out) + (((int64_t)lb * a.Hq + h0) * a.rows + r0 + t) * D;
+      p.dst = static_cast<T*>(a.q_out) + (((int64_t)lb * a.Hq + h0) * a.rows + r) * D;
       p.dst_step = (int64_t)a.rows * D;
       p.n = min(h1, nq) - h0;
       p.w = static_cast<const T*>(a.q_w);
     } else {
       const int off = which == 1 ? nq : nq + nk, h = max(h0 - off, 0);
       p.src = static_cast<const T*>(which == 1 ? a.k_in : a.v_in) + tok * (which == 1 ? a.k_stride : a.v_stride) + h * D;
-      p.dst = static_cast<T*>(which == 1 ? a.k_cache : a.v_cache) + (((int64_t)lb * a.Hkv + h) * a.cap + base + r0 + t) * D;
+      p.dst = static_cast<T*>(which == 1 ? a.k_cache : a.v_cache) + (((int64_t)lb * a.Hkv + h) * a.cap + base + r) * D;
       p.dst_step = a.cap * D;
       p.n = min(h1 - off, which == 1 ? nk : nv) - h;
       p.w = which == 1 ? static_cast<const T*>(a.k_w) : nullptr;
@@ -236,11 +246,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) q
   if (h0 < h1) load_heads<T, E>(x, part_of(start), 0, e0);
 
   const int half = a.rot_dim >> 1;
-  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
+  if (SHARED && !__syncthreads_or(ok)) return;
+  for (int i = threadIdx.x; i < TOK * half; i += kThreads) {
     const int tt = i / half, p = i - tt * half;
+    if (SHARED ? at[tt] == kNoToken : r - t + tt >= n) continue;
     const int axis = p < a.sec_end[0] ? 0 : p < a.sec_end[1] ? 1 : 2;
-    const double at = a.pos ? (double)a.pos[((int64_t)axis * a.B + b) * a.rows + r0 + tt] : (double)(base + r0 + tt);
-    double turns = at * a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
+    const int64_t x = SHARED ? at[tt] : (a.pos ? (int64_t)b * a.rows : base) + (r - t + tt);
+    const double where = a.pos ? (double)a.pos[(int64_t)axis * a.B * a.rows + x] : (double)x;
+    double turns = where * a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
     sincospif(2.f * (float)turns, &s, &c);
@@ -275,14 +288,21 @@ cudaError_t launch(const RopeArgs& a, int sms, cudaStream_t s) {
   const int64_t most = (int64_t)sms * (heads > kHeadsAtOnce ? 12 : 6) / 5;
   auto go = [&](auto tok) {
     constexpr int TOK = decltype(tok)::value;
-    const int chunks = (a.rows + TOK - 1) / TOK;
-    return launch_pdl(qk_norm_rope_kernel<T, E, TOK>, dim3((unsigned)((int64_t)a.L * a.B * chunks)), dim3(kThreads), 0, s,
-                      a, chunks, 1);
+    // Sequences of few tokens share CTAs where chunks of their own would leave more than a tenth of the places
+    // empty.  28 + 4 + 4 heads, d = 128, bf16, us with chunks of their own / shared: 1,024 sequences of one
+    // token 22.3 / 11.7, 28 layers x 64 sequences of one 42 / 17, 256 sequences of 9 26.4 / 17.9; where chunks
+    // are full the divisions and the table of tokens cost 2 in 100 (33,024 tokens 124.6 / 127.4).
+    const int64_t chunks = (a.rows + TOK - 1) / TOK;
+    if (10 * (chunks * TOK - a.rows) > chunks * TOK)
+      return launch_pdl(qk_norm_rope_kernel<T, E, TOK, true>, dim3((unsigned)((tokens + TOK - 1) / TOK)), dim3(kThreads), 0,
+                        s, a, (int)tokens, 1);
+    return launch_pdl(qk_norm_rope_kernel<T, E, TOK, false>, dim3((unsigned)((int64_t)a.L * a.B * chunks)), dim3(kThreads),
+                      0, s, a, (int)chunks, 1);
   };
   // one token: up to kHeadsAtOnce heads a CTA
   const int parts = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
   if (tokens * parts <= most)
-    return launch_pdl(qk_norm_rope_kernel<T, E, 1>, dim3((unsigned)(tokens * parts)), dim3(kThreads), 0, s, a, a.rows,
+    return launch_pdl(qk_norm_rope_kernel<T, E, 1, false>, dim3((unsigned)(tokens * parts)), dim3(kThreads), 0, s, a, a.rows,
                       parts);
   if (tokens <= 2 * most) return go(std::integral_constant<int, 2>());
   if (tokens <= 4 * most) return go(std::integral_constant<int, 4>());

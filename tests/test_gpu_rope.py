@@ -211,3 +211,20 @@ def test_no_rows_and_another_stream_and_a_graph():
     again = _run(c)
     torch.cuda.synchronize()
     assert torch.equal(got[0], again[0]) and torch.equal(got[1][:, :, :, 5:11], again[1][:, :, :, 5:11])
+
+
+@pytest.mark.parametrize("nB,rows,d,dtype", [(300, 1, 128, torch.bfloat16), (700, 3, 64, torch.bfloat16), (130, 5, 32, torch.float32)])
+def test_tokens_of_many_sequences_share_a_cta(nB, rows, d, dtype):
+    ragged = [(7 * b) % (rows + 1) for b in range(nB)]
+    lens = [(5 * b) % 11 for b in range(nB)]
+    ragged[3], lens[5] = -1, 1000                # one refused for its rows, one for the capacity, among others
+    c = _make(2, nB, rows, 6, 2, d, dtype, [min(x, 11) for x in lens], d, 3, 10, ragged=ragged, cap=11 + rows)
+    c["lens"] = lens
+    c["len"].copy_(torch.tensor(lens, dtype=torch.int32))
+    q, k, v, cv = _run(c)
+    cv.check()
+    assert B.std_get_device_error(clear=True) == B.STD_DEVERR_CAPACITY | B.STD_DEVERR_LENGTH
+    for b in (3, 5):
+        assert (q[:, b] == -7).all() and (k[:, b] == -7).all() and (v[:, b] == -7).all()
+    lens[5], c["n"][3], c["n"][5] = 0, 0, 0
+    _check(c, q, k, v)
