@@ -247,9 +247,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) q
 
   const int half = a.rot_dim >> 1;
   if (SHARED && !__syncthreads_or(ok)) return;
-  for (int i = threadIdx.x; i < TOK * half; i += kThreads) {
+  const int filled = SHARED ? TOK : min(TOK, n - (r - t));
+  for (int i = threadIdx.x; i < filled * half; i += kThreads) {
     const int tt = i / half, p = i - tt * half;
-    if (SHARED ? at[tt] == kNoToken : r - t + tt >= n) continue;
+    if (SHARED && at[tt] == kNoToken) continue;
     const int axis = p < a.sec_end[0] ? 0 : p < a.sec_end[1] ? 1 : 2;
     const int64_t x = SHARED ? at[tt] : (a.pos ? (int64_t)b * a.rows : base) + (r - t + tt);
     const double where = a.pos ? (double)a.pos[(int64_t)axis * a.B * a.rows + x] : (double)x;
