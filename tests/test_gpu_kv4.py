@@ -428,3 +428,52 @@ def test_calls_repeat_bit_for_bit_on_streams_and_in_graphs():
     torch.cuda.synchronize()
     assert torch.equal(graphs[0][1], _attend(dims, q, 1, c, cv, [4000, 234], 0))
     cv.check()
+
+
+@pytest.mark.parametrize("dtype,Hq,rows", [(torch.bfloat16, 7, 1), (torch.float32, 4, 1), (torch.bfloat16, 5, 7)])
+@pytest.mark.parametrize("power", [-40, 40])
+def test_values_of_any_stated_size(dtype, Hq, rows, power):
+    """Value rows of one constant (scale 0, where weights may grow largest) beside ordinary ones."""
+    n = 1500
+    dims, q, c, cv, cap = _attn_inputs(1, 1, Hq, 1, 128, rows, [n], 1, dtype, seed=11)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    v = torch.randn(1, 1, 1, cap, 128, generator=g, device="cuda")
+    v[..., ::2, :] = v[..., ::2, :1]
+    v = (v * 2.0 ** power).to(dtype)
+    B.std_kv4_quantize(dims, c, v, v, None, None, cap)
+    keep = c["v_codes"].clone(), c["v_scales"].clone()
+    k = torch.randn(1, 1, 1, cap, 128, generator=g, device="cuda").to(dtype)
+    B.std_kv4_quantize(dims, c, k, k, None, None, cap)
+    c["v_codes"].copy_(keep[0])
+    c["v_scales"].copy_(keep[1])
+    o = _attend(dims, q, rows, c, cv, [n], 1)
+    cv.check()
+    assert B.std_get_device_error() == 0
+    _check(o, q, c, [n], 1, dtype)
+
+
+@pytest.mark.parametrize("dtype,Hq,rows", [(torch.bfloat16, 7, 1), (torch.float32, 4, 1), (torch.bfloat16, 5, 7)])
+@pytest.mark.parametrize("power", [-100, 100])
+def test_queries_of_any_stated_size(dtype, Hq, rows, power):
+    """Tiny queries weigh all keys alike, huge ones take the key of the largest logit."""
+    n = 500
+    dims, q, c, cv, cap = _attn_inputs(1, 1, Hq, 1, 128, rows, [n], 1, dtype, seed=13)
+    q.copy_((torch.sign(q.float()) * 2.0 ** power).to(dtype))
+    o = _attend(dims, q, rows, c, cv, [n], 1)
+    cv.check()
+    assert B.std_get_device_error() == 0
+    if power < 0:
+        _check(o, q, c, [n], 1, dtype)
+        return
+    kc, ks, km = _parts(c, "k")
+    vc, vs, vm = _parts(c, "v")
+    K, V = O.kv4_values(kc, ks, km)[0, 0, 0], O.kv4_values(vc, vs, vm)[0, 0, 0]
+    sign = np.sign(q.double().cpu().numpy())[0, 0]
+    got = o.double().cpu().numpy()[0, 0]
+    for h in range(Hq):
+        for i in range(rows):
+            x = K[:n + 1 + i] @ sign[h, i]
+            top = np.argsort(x)[-2:]
+            # fp32 sums of 128 terms: a gap that their rounding cannot close decides the key
+            if x[top[1]] - x[top[0]] > 2 * (128 / 8 + 8) * 2.0 ** -22 * (np.abs(K).sum(1).max() + 16 * ks.max() * 128):
+                assert np.allclose(got[h, i], V[top[1]], rtol=torch.finfo(dtype).eps, atol=2.0 ** -10 * np.abs(V[top[1]]).max())
