@@ -477,3 +477,53 @@ def test_queries_of_any_stated_size(dtype, Hq, rows, power):
             # fp32 sums of 128 terms: a gap that their rounding cannot close decides the key
             if x[top[1]] - x[top[0]] > 2 * (128 / 8 + 8) * 2.0 ** -22 * (np.abs(K).sum(1).max() + 16 * ks.max() * 128):
                 assert np.allclose(got[h, i], V[top[1]], rtol=torch.finfo(dtype).eps, atol=2.0 ** -10 * np.abs(V[top[1]]).max())
+
+
+def test_many_rows_on_two_streams_and_in_graphs():
+    lens = [3000, 777]
+    dims, q, c, cv, _ = _attn_inputs(2, 2, 6, 1, 128, 9, lens, 1, torch.bfloat16, seed=14)
+    n = _i32(lens)
+    want = _attend(dims, q, 9, c, cv, n, 1)
+    _check(want, q, c, lens, 1, torch.bfloat16)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    need = B.std_kv4_attn_workspace_size(dims, 9, c["cap"])
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in side]
+    outs = [torch.zeros_like(q) for _ in range(8)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):                 # two calls at once, a workspace each
+        B.std_kv4_attn(dims, q, 9, c, n, 1, o, ws[i % 2], side[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    o, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.std_kv4_attn(dims, q, 9, c, n, 1, o, ws[0])
+        n.sub_(600)                              # what follows a call does not reach into it
+        B.std_kv4_attn(dims, q, 9, c, n, 1, outs[0], ws[0])
+        n.add_(600)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+    assert torch.equal(outs[0], _attend(dims, q, 9, c, cv, [2400, 177], 1))
+    cv.check()
+    assert B.std_get_device_error() == 0
+
+
+@pytest.mark.parametrize("nB,Hq,rows", [(1024, 2, 1), (333, 5, 5), (33, 3, 6)])
+def test_many_sequences(nB, Hq, rows):
+    lens = [(37 * b) % 211 for b in range(nB)]
+    dims, q, c, cv, cap = _attn_inputs(1, nB, Hq, 1, 64, rows, lens, 0, torch.bfloat16, seed=15)
+    o = _attend(dims, q, rows, c, cv, lens, 0)
+    cv.check()
+    assert B.std_get_device_error() == 0
+    _check(o, q, c, lens, 0, torch.bfloat16)
+    bad = list(lens)
+    bad[nB - 1], bad[7] = cap + 1, -1            # left as they are, the others as before
+    p = _attend(dims, q, rows, c, cv, bad, 0)
+    cv.check()
+    assert B.std_get_device_error(clear=True) == B.STD_DEVERR_LENGTH
+    ok = torch.ones(nB, dtype=torch.bool, device="cuda")
+    ok[7] = ok[nB - 1] = False
+    assert (p[:, ~ok] == -9).all()
+    _check(p[:, ok], q[:, ok], {k: (t[:, ok] if torch.is_tensor(t) else t) for k, t in c.items()},
+           [x for b, x in enumerate(lens) if b not in (7, nB - 1)], 0, torch.bfloat16)
