@@ -10,10 +10,10 @@
 // Both directions stream: 2 d values in, d + d / 8 bytes out for the K and V row of a head, and the
 // instructions on the way are what is hard to hide: at full HBM rate an SM has about 13 issue slots
 // for a bf16 channel.  When writing a lane holds 16 channels of a group (four lanes a group: two
-// shuffles for each extreme, and a group's scale is worked out four times, not eight), and a code
-// is nine float or integer instructions without a division, a conversion or a branch (code_word).
-// 143,616 rows of 4 heads, d = 128, bf16 (377 MB): written in 86.5 us, 17 instructions for a channel and 80% of
-// the issue slots used, read back in 61 us, 12.5 and 84%.
+// shuffles for each extreme, and a group's scale is worked out four times, not eight), and a code is
+// three instructions without a division, a conversion or a branch (code_word).
+// 143,616 rows of 4 heads, d = 128, bf16 (377 MB): written in 78.4 us (86.5 with nine instructions a code), read
+// back in 61.3.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -67,25 +67,30 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
-// Codes of 8 channels x - m >= 0, as one word.  c = floor(q) + (the rest is at least a half), q =
-// diff / s.  floor: adding 1.5 2^23 to diff / s with rounding down leaves it in the last bits; 1 / s is
-// good to 2^-23, so the floor is right except within 2^-19 of an integer, and there the comparison
-// below comes out the same from either side.  rest: diff - floor s is exact (floor s has 12 bits, and
-// its last bit and diff's are within 24 of the larger one); it counts as a half or more from s / 2 on
-// where the floor is odd and above s / 2 where it is even, and the bit pattern of s / 2 is even (s has
-// 8 bits), so "above" is one more in the last place.
-__device__ __forceinline__ uint32_t code_word(const float (&diff)[8], float s, float inv) {
-  const uint32_t half = __float_as_uint(0.5f * s);
-  uint32_t word = 0;
+// Codes of 8 channels, as one word, two channels an instruction: d = fl32(x - m), q = d / s, and 1.5 2^23 added
+// to q leaves its nearest integer, ties to even, in the last bits.  That is the exact quotient's rounding:
+// q0 = d (1 / s) is off by some units in the last place, its remainder d - q0 s is exact (s has 8 bits), and
+// q0 + remainder (1 / s) rounds to the quotient to nearest.  An exact tie T = k + 1/2 comes out as T (d = T s
+// has 13 bits).  A d next to T s is at least a unit in the last place off, so q is off by more than
+// 2^-24 (1 + 2^-8) of T, as s is at most 255/128 of a power of two; fp32 numbers that round to T are nearer.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float m, float s, float inv) {
+  const f32x2 m2 = f2_make(-m, -m), s2 = f2_make(-s, -s), i2 = f2_make(inv, inv), one = f2_make(12582912.f, 12582912.f);
+  uint32_t lo = 0, hi = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float t = __fmaf_rd(diff[i], inv, 12582912.f);
-    const uint32_t tb = __float_as_uint(t);
-    const float rest = fmaf(12582912.f - t, s, diff[i]);
-    const float over = rest - __uint_as_float(half | (~tb & 1u));
-    word = word * 16 + (tb + (uint32_t)(__float_as_int(over) >> 31));  // floor, or floor - 1 when below
+  for (int i = 3; i >= 0; --i) {
+    f32x2 d = f2_add(f2_make(x[i], x[i + 4]), m2);
+    float a, b;
+    if constexpr (CLAMP) {
+      f2_split(d, a, b);
+      d = f2_make(fmaxf(a, 0.f), fmaxf(b, 0.f));
+    }
+    const f32x2 q = f2_mul(d, i2);
+    f2_split(f2_add(f2_fma(f2_fma(q, s2, d), i2, q), one), a, b);
+    lo = lo * 16 + __float_as_uint(a);
+    hi = hi * 16 + __float_as_uint(b);
   }
-  return word - 0x11111111u * 0x4b3fffffu;  // the bits of 1.5 2^23, less one, in every place
+  return lo + hi * 65536 - 0x11111111u * 0x4b400000u;  // less the bits of 1.5 2^23 in every place
 }
 
 // The same for a scale so small that 1 / s or the products above leave the normal numbers: scaled up
@@ -170,20 +175,16 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, in
     const bool finite = fabsf(range) <= 3.402823466e38f;  // false for a NaN or an infinity
     uint32_t w0 = 0, w1 = 0;
     if (finite && s > 0.f) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float d = x[i / 8][i % 8] - m;
-        x[i / 8][i % 8] = sizeof(T) == 4 ? fmaxf(d, 0.f) : d;  // (bf16: m is the smallest x)
-      }
+constexpr bool CLAMP = sizeof(T) == 4;  // (bf16: m is the smallest x)
       if (s >= 7.888609052e-31f) {  // 2^-100
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        w0 = code_word(x[0], s, inv);
-        w1 = code_word(x[1], s, inv);
+        w0 = code_word<CLAMP>(x[0], m, s, inv);
+        w1 = code_word<CLAMP>(x[1], m, s, inv);
       } else {
         float y[16];  // (a copy: only this path's needs an address)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = x[i / 8][i % 8];
+        for (int i = 0; i < 16; ++i) y[i] = CLAMP ? fmaxf(x[i / 8][i % 8] - m, 0.f) : x[i / 8][i % 8] - m;
         w0 = code_word_tiny(y, s);
         w1 = code_word_tiny(y + 8, s);
       }

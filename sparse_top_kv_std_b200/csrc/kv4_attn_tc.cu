@@ -103,11 +103,6 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // tcgen05.mma and its commit by the lane whose `leader` is set; the other operands are the warp's.
 __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t add) {
   asm volatile(
