@@ -12,8 +12,8 @@
 // for a bf16 channel.  When writing a lane holds 16 channels of a group (four lanes a group: two
 // shuffles for each extreme, and a group's scale is worked out four times, not eight), and a code is
 // three instructions without a division, a conversion or a branch (code_word).
-// 143,616 rows of 4 heads, d = 128, bf16 (377 MB): written in 78.4 us (86.5 with nine instructions a code), read
-// back in 61.3.
+// 143,616 rows of 4 heads, d = 128, bf16 (377 MB): written in 72.9 us (86.5 with nine instructions a
+// code; 78.4 with three CTAs an SM), read back in 58.2, the rate of a copy (61.3 with 8 channels a lane).
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -123,7 +123,7 @@ __device__ __forceinline__ bool row_span(const Kv4Args& a, int b, RowSpan* sp) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Args a, int chunks) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) kv4_write_kernel(const Kv4Args a, int chunks) {
   constexpr int GR = D / kKv4Group;
   constexpr int LPR = D / 16;          // lanes of a row: word pairs (2 j, 2 j + 1) of one group
   constexpr int RPB = kThreads / LPR;  // rows of a CTA at a time
@@ -208,7 +208,8 @@ constexpr bool CLAMP = sizeof(T) == 4;  // (bf16: m is the smallest x)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Args a, int chunks) {
-  constexpr int LPR = D / 8;
+  constexpr int GR = D / kKv4Group;
+  constexpr int LPR = D / 16;  // a lane reads two words of a row: at d = 128 one of each group
   constexpr int RPB = kThreads / LPR;
   pdl_wait();  // memory of earlier kernels in the stream is visible from here on
   pdl_trigger();
@@ -221,43 +222,55 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Args a, int
     if (chunk == 0 && which == 0 && threadIdx.x == 0) flag_error(a.err, STD_DEVERR_CAPACITY);
     return;
   }
-  T* dst = const_cast<T*>(static_cast<const T*>(which ? a.v : a.k));
-  const uint32_t* codes = static_cast<const uint32_t*>(which ? a.v_codes : a.k_codes);
-  const uint32_t* scales = static_cast<const uint32_t*>(which ? a.v_scales : a.k_scales);
-  const int w = threadIdx.x % LPR, grp = D == 128 ? w & 1 : 0;
-  const int ch = kv4_word_channel<D>(w);
-  const int r0 = chunk * RPB * kUnroll + threadIdx.x / LPR;
-  uint32_t word[kUnroll], sc[kUnroll];
+  const int w = threadIdx.x % LPR;
+  const int r0 = chunk * (RPB * kUnroll) + threadIdx.x / LPR;
+  T* dst = const_cast<T*>(static_cast<const T*>(which ? a.v : a.k)) + (int64_t)prob * a.rows_cap * D;
+  const int64_t first = (int64_t)prob * a.cap + sp.pos;
+  const uint32_t* codes = static_cast<const uint32_t*>(which ? a.v_codes : a.k_codes) + first * (D / 8) + 2 * w;
+  const uint32_t* scales = static_cast<const uint32_t*>(which ? a.v_scales : a.k_scales) + first * GR;
+  uint2 word[kUnroll];
+  uint32_t sc[kUnroll][GR];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int r = r0 + u * RPB;
-    word[u] = sc[u] = 0;
     if (r < sp.n && STD_DCHECK(sp.pos + r < a.cap, a.err)) {
-      const int64_t row = (int64_t)prob * a.cap + sp.pos + r;
-      word[u] = __ldcs(codes + row * LPR + w);
-      sc[u] = __ldg(scales + row * (D / kKv4Group) + grp);
+      word[u] = __ldcs(reinterpret_cast<const uint2*>(codes + (int64_t)r * (D / 8)));
+      if constexpr (GR == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(scales + (int64_t)r * 2));
+        sc[u][0] = x.x; sc[u][1] = x.y;
+      } else {
+        sc[u][0] = __ldg(scales + r);
+      }
     }
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int r = r0 + u * RPB;
-    if (r >= sp.n || !STD_DCHECK(r < a.rows_cap, a.err)) break;
-    const float s = __uint_as_float(sc[u] << 16), m = __uint_as_float(sc[u] & 0xffff0000u);
-    // 2^23 + c, one byte permutation, less 2^23
-    const uint32_t even = word[u] & 0x0f0f0f0fu, odd = (word[u] >> 4) & 0x0f0f0f0fu;
-    float x[8];
+    if (r >= sp.n || !STD_DCHECK(r < a.rows_cap && sp.pos + r < a.cap, a.err)) return;
+    float x[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t f = __byte_perm(i & 1 ? odd : even, 0x4b000000u, 0x7550 + i / 2);
-      x[i] = fmaf(__uint_as_float(f) - 8388608.f, s, m);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t c = i ? word[u].y : word[u].x, sm = sc[u][GR == 2 ? i : 0];
+      const float s = __uint_as_float(sm << 16), m = __uint_as_float(sm & 0xffff0000u);
+      // 2^23 + c, one byte permutation, less 2^23
+      const uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const f32x2 f = f2_add(f2_make(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7550 + k)),
+                                       __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7550 + k))),
+                               f2_make(-8388608.f, -8388608.f));
+        f2_split(f2_fma(f, f2_make(s, s), f2_make(m, m)), x[i][2 * k], x[i][2 * k + 1]);
+      }
     }
-    store8<T>(dst + ((int64_t)prob * a.rows_cap + r) * D + ch, x);
+    T* row = dst + (int64_t)r * D;
+    store8<T>(row + kv4_word_channel<D>(2 * w), x[0]);
+    store8<T>(row + kv4_word_channel<D>(2 * w + 1), x[1]);
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(const Kv4Args& a, bool read, cudaStream_t s) {
-  const int per_cta = kThreads / (D / (read ? 8 : 16)) * kUnroll;
+  const int per_cta = kThreads / (D / 16) * kUnroll;
   const int chunks = (a.max_n + per_cta - 1) / per_cta;
   const dim3 grid((unsigned)(2 * (int64_t)a.L * a.B * a.Hkv * chunks));
   if (read) return launch_pdl(kv4_read_kernel<T, D>, grid, dim3(kThreads), 0, s, a, chunks);
