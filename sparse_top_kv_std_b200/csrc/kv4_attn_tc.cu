@@ -13,9 +13,8 @@
 // barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
-// x 4 heads x 33,024 keys, 49 rows, 403 us (four blocks of 16 rows in kv4_attn.cu: 728 us), 3,700 clocks a
-// tile.  In them the tensor cores are busy 800, the warps' shared-memory traffic (widened rows, weights,
-// tables) takes 1,940 and the issue slots are 55% used: what bounds a tile is that its phases follow each other.
+// x 4 heads x 33,024 keys, 49 rows, 368 us (four blocks of 16 rows in kv4_attn.cu: 728 us; 403 where a thread
+// widens a group of its key of K and not half a row, which reads all codes twice).  Of a tile's some 3,400 clocks the tensor cores are busy 800; the phases follow each other.
 #include "kv4_attn.cuh"
 
 #include <cuda_fp16.h>
@@ -31,8 +30,10 @@ constexpr int kThreads = kTile * kRows / kShare;
 constexpr int kStages = 4;
 // The thread that fetches tiles, and the warps that issue the products: of those that widen K, which is less
 // work than V.  (The issue of P V blocks its warp until the tensor cores have taken most of it, some 800
-// clocks; wg 3 has the fewest rows where a block is short.)
-constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 12;
+// clocks; wg 3 has the fewest rows where a block is short.  On the S issuer's scheduler, warp 12, it is 377 us
+// where this is 368.)
+constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 13;
+static_assert(kIssueS != kIssuePV && kIssueS != kFetcher / 32 && kIssuePV != kFetcher / 32, "one role a warp");
 constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
 constexpr float kSmall = 9.094947e-13f;
 constexpr float kHeadroom = 8.f;
@@ -150,26 +151,33 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
 // take codes out of a word, (0, 4), (1, 5), (2, 6), (3, 7); the second and fourth pair come at 2^-20.
 __device__ __forceinline__ constexpr int perm8(int p) { return (p >> 1) + 4 * (p & 1); }
 
-// One group of a thread's key of K to tensor memory (its lane), 32 columns.
+// Four columns: a word of K.
+__device__ __forceinline__ void widen_word(uint32_t x, uint32_t* r) {
+  r[0] = widen0(x);
+  r[1] = widen4(x);
+  r[2] = widen0(x >> 8);
+  r[3] = widen4(x >> 8);
+}
+// Half of a thread's key of K to tensor memory (its lane), 16 columns a group.
 template <int D>
-__device__ __forceinline__ void widen_k(uint32_t row, uint32_t taddr, int gr) {
-  constexpr int GR = D / kKv4Group;
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const uint4 v = lds128(row + 16 * i);
+__device__ __forceinline__ void widen_k(uint32_t row, uint32_t taddr, int key, int part) {
+  uint32_t r[16];
+  if constexpr (D == 64) {
+    const uint4 v = lds128(row + 16 * part);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; k += GR) {
-      const uint32_t x = GR == 2 && gr ? w[k + GR - 1] : w[k];
-      const int j = 4 * ((4 * i + k) / GR);
-      r[j] = widen0(x);
-      r[j + 1] = widen4(x);
-      r[j + 2] = widen0(x >> 8);
-      r[j + 3] = widen4(x >> 8);
-    }
+    for (int k = 0; k < 4; ++k) widen_word(w[k], r + 4 * k);
+    tc::tmem_st_x16(taddr + 16 * part, r);
+    return;
   }
-  tc::tmem_st_x32(taddr, r);
+  const uint4 lo = lds128(row + 32 * part), hi = lds128(row + 32 * part + 16);
+  const uint32_t w[8] = {lo.x, lo.z, hi.x, hi.z, lo.y, lo.w, hi.y, hi.w};
+#pragma unroll
+  for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) widen_word(w[4 * gr + k], r + 4 * k);
+    tc::tmem_st_x16(taddr + 32 * gr + 16 * part, r);
+  }
 }
 
 // Half of a thread's key of V to its 128-byte rows of the operand, chunk c of 16 bytes at c ^ (key % 8).
@@ -351,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       commit(leader, &ctl.pv_done[odd]);
     };
 
-    // Threads that widen K: wg 0 (group 0) and 3 (group 1); V: 1 and 2, half a row each.
-    const bool k_side = wg == 0 || (GR == 2 && wg == 3);
+    // Threads that widen K: wg 0 and 3; V: 1 and 2, half a row each.
+    const bool k_side = wg == 0 || wg == 3;
     auto widen_keys = [&](int i) {
       if (k_side) {
-        widen_k<D>(stage_of(i) + key * At::CW, lanes + C::K + (i & 1) * GR * 32 + (wg == 3 ? 32 : 0), wg == 3);
+        widen_k<D>(stage_of(i) + key * At::CW, lanes + C::K + (i & 1) * GR * 32, key, wg == 3);
         tc::tmem_st_wait();
       }
     };
