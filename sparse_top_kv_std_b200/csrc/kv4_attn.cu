@@ -734,8 +734,8 @@ cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
 
 // More than 16 query rows share a widened code often enough for the tensor-memory kernel (bf16; fp32
 // queries need their second fp16 term, and two weights for one, and stay here).  28 layers x 4 heads x
-// 33,024 keys, there / here: 16 rows 322 / 192 us, 18 rows 330 / 370, 28 rows 369 / 372, 49 rows 402 / 728.
-// (One layer of 16,512 keys: 18 rows 18.8 / 17.8, 28 rows 19.6 / 18.7, 49 rows 22.5 / 24.7.)
+// 33,024 keys, there / here: 16 rows 288 / 192 us, 18 rows 296 / 370, 28 rows 332 / 373, 49 rows 367 / 727.
+// (One layer of 16,512 keys: 18 rows 18.2 / 17.9, 28 rows 18.9 / 18.6, 49 rows 21.9 / 24.6.)
 static bool on_tensor_memory(const Kv4AttnArgs& a) { return a.dtype == STD_BF16 && a.rows > 16; }
 
 // Query rows of a block, and CTAs of an SM, by the kernel the call takes.
