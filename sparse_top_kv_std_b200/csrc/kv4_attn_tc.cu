@@ -14,7 +14,7 @@
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
 // x 4 heads x 33,024 keys, 49 rows, 368 us (four blocks of 16 rows in kv4_attn.cu: 727 us; 403 where a thread
-// widens a group of its key of K and not half a row, which reads all codes twice).  Of a tile's some 3,400 clocks the tensor cores are busy 800; the phases follow each other.
+// widens a group of its key of K and not half a row, which reads all codes twice).  Of a tile's 3,350 clocks the tensor cores are busy 800; the phases follow each other.
 #include "kv4_attn.cuh"
 
 #include <cuda_fp16.h>
