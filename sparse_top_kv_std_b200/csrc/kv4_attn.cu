@@ -171,9 +171,9 @@ struct State {
   static constexpr int KS = D / 16;          // k-steps of S^T
   static constexpr int GR = D / kKv4Group;   // groups
   static constexpr int MT = D / 16;          // 16-channel tiles of O^T
-  // The queries, scaled by a power of two, are B operands in shared memory, four registers of a lane
+  // The queries, each row scaled by a power of two, are B operands in shared memory, four registers of a lane
   // together: [NT][KS / 2][32 lanes][4], and for fp32 queries what is below fp16 behind them.
-  float back;                                // K's scales times this: undoes q's scaling, log2(e) / sqrt(d)
+  float back[NT][2];                         // a row's power of two: undoes its scaling
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
   // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8); fp32 queries: sum (p sv) (b - 8)
@@ -188,10 +188,11 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
   const int g = lane >> 2, t = lane & 3;
   constexpr int WPL = D / 32;  // words of a row that lane t multiplies
   float x[NT][WPL][8];
-  float top = 0.f;
+  float mul[NT], back[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = u.rb * 8 * NT + nt * 8 + g;
+    float top = 0.f;
 #pragma unroll
     for (int w = 0; w < WPL; ++w) {
       const int ch = kv4_word_channel<D>(WPL * t + w);
@@ -216,16 +217,16 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       for (int i = 0; i < 8; ++i)
         if (fabsf(y[i]) < INFINITY) top = fmaxf(top, fabsf(y[i]));  // (a row with an infinity gives NaN by itself)
     }
+    // Scale each row by a power of two of its own, so that it keeps its bits whatever the other rows of the
+    // block hold: its largest entry lies in [2^14, 2^15), a sixteenth of that where it meets codes at 2^-20.
+    // That is exact, and bf16 entries down to 2^-27 of it keep all their bits.  Products come out in units of
+    // 2^(ex - 14).
+    top = quad_max(top);
+    int ex = (int)(__float_as_uint(top) >> 23) - 127;
+    ex = ex < -100 ? -100 : ex;
+    mul[nt] = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+    back[nt] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
   }
-  top = warp_max(top);
-  // Scale the block by a power of two that puts its largest entry in [2^14, 2^15), a sixteenth of that
-  // where it meets codes at 2^-20: exact, and entries down to 2^-24 of it keep all their bits.
-  int ex = (int)(__float_as_uint(top) >> 23) - 127;
-  ex = ex < -100 ? -100 : ex;
-  const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-  // the products come out in units of 2^(ex - 14), and 2^24 where the codes are subnormals
-  st.back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-  if constexpr (!F32) st.back *= 16777216.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float sum[S::GR];
@@ -236,7 +237,7 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       float(&y)[8] = x[nt][w];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        y[i] *= mul;
+        y[i] *= mul[nt];
         sum[S::GR == 2 ? (w & 1) : 0] += y[i];
       }
       if (store) {
@@ -261,6 +262,7 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       const int from = 4 * (2 * t + e);  // a lane that holds row 2 t + e
 #pragma unroll
       for (int gr = 0; gr < S::GR; ++gr) st.qsum[nt][gr][e] = __shfl_sync(0xffffffffu, sum[gr], from);
+      st.back[nt][e] = __shfl_sync(0xffffffffu, back[nt], from);
       st.M[nt][e] = -INFINITY;
       st.l[nt][e] = 0.f;
 #pragma unroll
@@ -331,10 +333,12 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
         lim[nt][e] = n0 + (row < rows ? row % nq : 0);
       }
   }
-  // The 16 keys' scales to fp32, one half-warp for K and one for V, (s, m) of both groups: each lane
-  // needs two keys' of each, and four lanes the same ones.
+  // The 16 keys' scales to fp32, one half-warp for K (with log2(e) / sqrt(d), and 2^24 where codes are
+  // subnormals) and one for V, (s, m) of both groups: each lane needs two keys' of each, and four lanes the
+  // same ones.
   {
-    const float c = lane < 16 && !F32 ? 0.f : 8.f, f = lane < 16 ? st.back : 1.f;
+    const float c = lane < 16 && !F32 ? 0.f : 8.f;
+    const float f = lane < 16 ? kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f) * (F32 ? 1.f : 16777216.f) : 1.f;
     if constexpr (GR == 2) {
       const uint2 u = lds64(at.scale + tile);
       const float s0 = lo_bf16(u.x), s1 = lo_bf16(u.y);
@@ -406,17 +410,20 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
   // reference is set yet) the references of this warp's rows move up and the weights are taken again.
   float p[NT][4], wt[NT][GR][4], l[NT][2];
   bool seen[NT][4];
+  auto dot = [&](int nt, int i) {  // the logit but for the row's power of two
+    float x = mk[i >> 1][0] * st.qsum[nt][0][i & 1];
+    x = fmaf(sk[i >> 1][0], acc[nt][0][i], x);
+    if constexpr (GR == 2) {
+      x = fmaf(mk[i >> 1][1], st.qsum[nt][1][i & 1], x);
+      x = fmaf(sk[i >> 1][1], acc[nt][1][i], x);
+    }
+    return x;
+  };
   auto weigh = [&](int nt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int hf = i >> 1, e = i & 1;
-      float x = -st.M[nt][e];
-#pragma unroll
-      for (int gr = 0; gr < GR; ++gr) {
-        x = fmaf(mk[hf][gr], st.qsum[nt][gr][e], x);
-        x = fmaf(sk[hf][gr], acc[nt][gr][i], x);
-      }
-      p[nt][i] = ex2(x);
+      p[nt][i] = ex2(fmaf(dot(nt, i), st.back[nt][e], -st.M[nt][e]));
       if constexpr (MASK) {
         seen[nt][i] = key0 + kap + 8 * hf < lim[nt][e];
         if (!seen[nt][i]) p[nt][i] = 0.f;
@@ -450,12 +457,9 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
         float z = -INFINITY;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float x = 0.f;
-#pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
-            x = fmaf(sk[hf][gr], acc[nt][gr][2 * hf + e], fmaf(mk[hf][gr], st.qsum[nt][gr][e], x));
           const float big_s = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
-          if (!MASK || seen[nt][2 * hf + e]) z = fmaxf(z, x + __log2f(big_s));
+          if (!MASK || seen[nt][2 * hf + e])
+            z = fmaxf(z, fmaf(dot(nt, 2 * hf + e), st.back[nt][e], __log2f(big_s)));
         }
         z = column_max(z);
         if (z - st.M[nt][e] > 14.9f) {

@@ -51,7 +51,7 @@ struct Lay {
   static constexpr int Q_GROUP = kRows * 128;
   static constexpr int RING = Q + GR * Q_GROUP;
   static constexpr int TAB = RING + kStages * TileAt<D>::BYTES;
-  static constexpr int RED = TAB + 5 * kRows * 4;         // [4 warps][64 rows][3]
+  static constexpr int RED = TAB + 6 * kRows * 4;         // [4 warps][64 rows][3]
   static constexpr int BYTES = RED + 4 * kRows * 3 * 4;
 };
 
@@ -60,7 +60,6 @@ struct Ctl {
   Split split;
   Fetch fetch;
   uint32_t tmem;
-  float qmax[kThreads / 32];
   volatile int abort;
 };
 
@@ -202,11 +201,10 @@ __device__ __forceinline__ void widen_v(uint32_t row, uint32_t dst, int key, int
   }
 }
 
-// A block's queries: the operand (kRows x 64 for each group, fp16, scaled by a power of two, K-major with
-// swizzled rows), the group sums of the scaled queries and the factor that undoes the scaling.
+// A block's queries: the operand (kRows x 64 for each group, fp16, each row scaled by a power of two of its own, K-major
+// with swizzled rows), and the rows' tables: the group sums of the scaled queries and the powers of two that undo it.
 template <int D>
-__device__ __forceinline__ float load_queries(const Kv4AttnArgs& a, const Unit& u, int n0, Ctl* ctl, uint8_t* smem,
-                                              int tid) {
+__device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Unit& u, int n0, uint8_t* smem, int tid) {
   constexpr int GR = D / kKv4Group, NC = D / 8;  // channels of a thread: an eighth of a row
   const int r = tid >> 3, part = tid & 7, row = u.rb * kRows + r;
   float x[NC];
@@ -222,15 +220,11 @@ __device__ __forceinline__ float load_queries(const Kv4AttnArgs& a, const Unit& 
     for (int k = 0; k < 8; ++k)
       if (fabsf(x[i + k]) < INFINITY) top = fmaxf(top, fabsf(x[i + k]));
   }
-  top = warp_max(top);
-  if ((tid & 31) == 0) ctl->qmax[tid >> 5] = top;
-  __syncthreads();
-  top = warp_max(ctl->qmax[tid & (kThreads / 32 - 1)]);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   int ex = (int)(__float_as_uint(top) >> 23) - 127;
   ex = ex < -100 ? -100 : ex;
   const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-  float back = kLog2e * rsqrtf((float)D) * __uint_as_float((uint32_t)((ex > 100 ? ex - 10 : ex + 10) + 127) << 23);
-  if (ex > 100) back *= 1048576.f;
   float sum = 0.f;
   const int per = 8 / GR, gr = part / per, c0 = part % per * NC;  // threads of a group; channels of the group
   uint8_t* base = smem + Lay<D>::Q + gr * Lay<D>::Q_GROUP + r * 128;
@@ -254,8 +248,8 @@ __device__ __forceinline__ float load_queries(const Kv4AttnArgs& a, const Unit& 
   if (part == 1) {
     tab[2 * kRows + r] = INFINITY;  // minus the row's reference
     reinterpret_cast<int*>(tab)[4 * kRows + r] = n0 + (row < a.rows ? row % a.nq : 0);  // keys it attends
+    tab[5 * kRows + r] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
   }
-  return back;
 }
 
 template <int D>
@@ -296,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   const int64_t begin64 = (int64_t)share * blockIdx.x;
   const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
   const uint32_t ring = sm + L::RING;
-  float* tab = reinterpret_cast<float*>(smem + L::TAB);  // sums of q (two groups), minus the references, factors
+  // of the rows: sums of q (two groups), minus the references, factors, keys they attend, powers of two
+  float* tab = reinterpret_cast<float*>(smem + L::TAB);
   float* red = reinterpret_cast<float*>(smem + L::RED);
   if (tid == kFetcher && begin < end) {
     ctl.fetch.next = begin;
@@ -318,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const int n = min(u.groups - u.first, end - t);
     const int nt = min(n * group, (keys + kTile - 1) / kTile - first);  // (may be none)
     const int n0 = keys - a.nq + 1;
-    const float back = load_queries<D>(a, u, n0, &ctl, smem, tid);
+    load_queries<D>(a, u, n0, smem, tid);
     f32x2 l[kShare / 2], pm[GR][kShare / 2];  // sums of p and of p (mv + 8 sv), two rows together
 #pragma unroll
     for (int j = 0; j < kShare / 2; ++j) {
@@ -395,14 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       if (i + 1 < nt) widen_keys(i + 1);
       if (wg == 1 || wg == 2) widen_v<D>(cur + At::VC + key * At::CW, sm + L::V + buf * GR * L::V_GROUP, key, wg - 1);
 
-      // this thread's key: scales (K's with the factor that undoes the queries'), position
+      // this thread's key: scales (K's with log2(e) / sqrt(d), and 2^24 as codes are subnormals), position
+      constexpr float kBack = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f) * 16777216.f;
       const int pos = (first + i) * kTile + key;
       float sk[GR], mk[GR], sv[GR], mv[GR], smax = kSmall;
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
         const uint32_t uk = lds32(cur + At::KS + key * At::SW + 4 * gr), uv = lds32(cur + At::VS + key * At::SW + 4 * gr);
-        sk[gr] = lo_bf16(uk) * back;
-        mk[gr] = hi_bf16(uk) * back;
+        sk[gr] = lo_bf16(uk) * kBack;
+        mk[gr] = hi_bf16(uk) * kBack;
         sv[gr] = lo_bf16(uv);
         mv[gr] = fmaf(8.f, sv[gr], hi_bf16(uv));
         smax = fmaxf(smax, sv[gr]);
@@ -435,10 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
             f32x2 x[4];
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {  // rows 2 k .. 2 k + 3
-              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(at + 2 * kRows + 2 * k);
               const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(at + 2 * k);
-              x[k] = f2_fma(f2_make(mk[0], mk[0]), q0.x, m.x);
-              x[k + 1] = f2_fma(f2_make(mk[0], mk[0]), q0.y, m.y);
+              x[k] = f2_mul(f2_make(mk[0], mk[0]), q0.x);
+              x[k + 1] = f2_mul(f2_make(mk[0], mk[0]), q0.y);
               if constexpr (GR == 2) {
                 const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(at + kRows + 2 * k);
                 x[k] = f2_fma(f2_make(mk[1], mk[1]), q1.x, x[k]);
@@ -453,6 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
               for (int gr = 0; gr < GR; ++gr)
                 x[k] = f2_fma(f2_make(sk[gr], sk[gr]),
                               f2_make(__uint_as_float(s[gr][2 * k]), __uint_as_float(s[gr][2 * k + 1])), x[k]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(at + 2 * kRows + 2 * k);
+              const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(at + 5 * kRows + 2 * k);
+              x[k] = f2_fma(x[k], b.x, m.x);
+              x[k + 1] = f2_fma(x[k + 1], b.y, m.y);
+            }
             if (edge) {
               const int* lim = reinterpret_cast<const int*>(at) + 4 * kRows;
 #pragma unroll
@@ -538,10 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int row = row0 + k;
-            float x = 0.f;
+            float x = mk[0] * tab[row];  // (the sum above, in its order)
+            if constexpr (GR == 2) x = fmaf(mk[1], tab[kRows + row], x);
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), fmaf(mk[gr], tab[gr * kRows + row], x));
-            const float z = warp_max(pos < reinterpret_cast<const int*>(tab)[4 * kRows + row] ? x + ls : -INFINITY);
+            for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), x);
+            x = fmaf(x, tab[5 * kRows + row], ls);
+            const float z = warp_max(pos < reinterpret_cast<const int*>(tab)[4 * kRows + row] ? x : -INFINITY);
             if (lane == 0) red[qd * kRows + row] = z;
           }
         }
