@@ -45,8 +45,11 @@ namespace {
 constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLimit = 32768.f;        // largest weight x scale that goes to fp16
-constexpr float kSmall = 9.094947e-13f;  // 2^-40: scales below it count as this much, so that p stays below 2^55
-constexpr float kMostSum = 1.2676506e30f;  // 2^100: a sum of weights above it moves the reference too
+constexpr float kSmall = 9.094947e-13f;  // 2^-40: scales below it count as this much when a reference moves
+// 2^70: a sum of weights above it moves the reference too, where scales are so small (0, for constant values) that
+// weight x scale never does.  Minima are below 2^41 in magnitude (values up to 2^40), so that sum p (mv + 8 sv) of a
+// lane stays below 2^111, and of all warps and CTAs below 2^122.
+constexpr float kMostSum = 1.1805916e21f;
 constexpr float kHeadroom = 8.f;         // a new reference puts the largest one at 2^8
 
 // ---------------------------------------------------------------- shared memory

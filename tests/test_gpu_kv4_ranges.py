@@ -170,3 +170,29 @@ def test_rows_of_any_bits_behind_the_valid_ones(G, rows):
     q.view(G * rows, 128)[torch.from_numpy(junk).cuda()] = bits.view(torch.bfloat16)
     o, q, c = _attend(q, _randn(6, 1, 1, 1, 528, 128), _randn(7, 1, 1, 1, 528, 128), rows, lens, torch.bfloat16)
     _check(o, np.where(np.isfinite(q), q, 0), c, lens, torch.bfloat16, skip=junk)
+
+
+# ----------------------------------------------------------------------------- sums of weights and minima
+
+def _steps(q_sign, cap, d, height):
+    """Keys along q_sign [d] whose logits (for queries q_sign) rise by `height` in log2 units with every tile of 128
+    keys, five tiles long, then start again."""
+    level = (torch.arange(cap, device="cuda") // 128 % 5).float() * height * np.log(2) / np.sqrt(d)
+    return q_sign * level[:, None]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,rows", HEADS[:3])
+@pytest.mark.parametrize("power", [20, 36, 40])
+def test_constant_values_with_rising_logits(dtype, d, G, rows, power):
+    """Value rows of one constant have scale 0, so that no weight times scale ever grows: the sum of weights
+    times minima has to stay finite by itself."""
+    L, Hkv, n = 6, 8, 2000
+    sign = torch.sign(_randn(8, d))
+    k = _steps(sign, n + 16 + rows // 16 * 16, d, 45).expand(L, 1, Hkv, -1, d)
+    cap = k.shape[3]
+    v = (2.0 ** power * (1 + torch.arange(cap, device="cuda") % 7 / 8.)).view(1, 1, 1, cap, 1).expand(L, 1, Hkv, cap, d)
+    q = sign.expand(L, 1, G * Hkv, rows, d)
+    o, q, c = _attend(q.contiguous(), k.contiguous(), v.contiguous(), rows, [n], dtype)
+    _check(o, q, c, [n], dtype)
