@@ -6,7 +6,8 @@
 //   o_rc = [ sum_j (p_rj sv_jg) (b_jc - 8) + sum_j p_rj (mv_jg + 8 sv_jg) ] / sum_j p_rj,   p = 2^(x - M_r)
 //
 // so the scales never touch the codes: K's multiply the two partial dot products of a key, V's
-// multiply the weights.  A code enters the tensor cores as the fp16 number whose bits are the masked
+// multiply the weights (with a factor of the row's and group's own, undone at the end, which keeps the products in
+// fp16's range).  A code enters the tensor cores as the fp16 number whose bits are the masked
 // code: a subnormal, c 2^-24 (low nibble of a byte) or c 2^-20 (high), exact in the product and in the
 // fp32 sum; powers of two in q and in the result undo it.  One mask for two codes is all that widening
 // costs.  (The sum over keys has to be centred, b - 8, because sum p b grows without bound while the
@@ -44,13 +45,13 @@ namespace {
 
 constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLimit = 32768.f;        // largest weight x scale that goes to fp16
-constexpr float kSmall = 9.094947e-13f;  // 2^-40: scales below it count as this much when a reference moves
+constexpr float kLimit = 32768.f;        // largest weight x scale x factor that goes to fp16
+constexpr float kMostFactor = 1.3292280e36f;  // 2^120: a factor of weights x scales before any was seen
 // 2^70: a sum of weights above it moves the reference too, where scales are so small (0, for constant values) that
 // weight x scale never does.  Minima are below 2^41 in magnitude (values up to 2^40), so that sum p (mv + 8 sv) of a
 // lane stays below 2^111, and of all warps and CTAs below 2^122.
 constexpr float kMostSum = 1.1805916e21f;
-constexpr float kHeadroom = 8.f;         // a new reference puts the largest one at 2^8
+constexpr float kHeadroom = 8.f;         // a new reference puts the largest weight at 2^8
 
 // ---------------------------------------------------------------- shared memory
 template <int D, int NT, bool F32>
@@ -179,9 +180,12 @@ struct State {
   float back[NT][2];                         // a row's power of two: undoes its scaling
   float qsum[NT][GR][2];                     // sum of the scaled q over a group
   float M[NT][2], l[NT][2], pm[NT][GR][2];   // reference, sum p, sum p (mv + 8 sv)
-  // sum (p sv) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8); fp32 queries: sum (p sv) (b - 8)
+  // A group's weights x scales times this go to fp16.  It puts the row's largest in that group at 2^7 to 2^15, so
+  // that they keep their 11 bits (or 2^-32 of the largest) whatever the sizes of the other group and of the minima.
+  float factor[NT][GR][2];
+  // sum (p sv factor) b, in units of 2^-24 (rows g) and 2^-20 (rows g + 8); fp32 queries: sum (p sv factor) (b - 8)
   float o[NT][MT][4];
-  float eight[F32 ? 1 : NT][GR][4];          // sum (p sv) 8 of the same keys since the last settle(), same units
+  float eight[F32 ? 1 : NT][GR][4];          // sum (p sv factor) 8 of the same keys since the last settle(), same units
 };
 
 template <int D, int NT, bool F32>
@@ -269,7 +273,10 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
       st.M[nt][e] = -INFINITY;
       st.l[nt][e] = 0.f;
 #pragma unroll
-      for (int gr = 0; gr < S::GR; ++gr) st.pm[nt][gr][e] = 0.f;
+      for (int gr = 0; gr < S::GR; ++gr) {
+        st.pm[nt][gr][e] = 0.f;
+        st.factor[nt][gr][e] = kMostFactor;
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -409,8 +416,8 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
   }
 
   // Logits and weights against the running reference M.  Element i of an accumulator: key half
-  // i / 2, row 2 t + i % 2.  w = p sv has to fit fp16 and the sum of p fp32; where they do not (or no
-  // reference is set yet) the references of this warp's rows move up and the weights are taken again.
+  // i / 2, row 2 t + i % 2.  w = p sv factor has to fit fp16 and the sum of p fp32; where they do not (or no
+  // reference is set yet) this warp's references move up, factors move, and the weights are taken again.
   float p[NT][4], wt[NT][GR][4], l[NT][2];
   bool seen[NT][4];
   auto dot = [&](int nt, int i) {  // the logit but for the row's power of two
@@ -422,27 +429,31 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
     }
     return x;
   };
-  auto weigh = [&](int nt) {
+  auto probabilities = [&](int nt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int hf = i >> 1, e = i & 1;
-      p[nt][i] = ex2(fmaf(dot(nt, i), st.back[nt][e], -st.M[nt][e]));
+      p[nt][i] = ex2(fmaf(dot(nt, i), st.back[nt][i & 1], -st.M[nt][i & 1]));
       if constexpr (MASK) {
-        seen[nt][i] = key0 + kap + 8 * hf < lim[nt][e];
+        seen[nt][i] = key0 + kap + 8 * (i >> 1) < lim[nt][i & 1];
         if (!seen[nt][i]) p[nt][i] = 0.f;
-      }
-#pragma unroll
-      for (int gr = 0; gr < GR; ++gr) {
-        wt[nt][gr][i] = p[nt][i] * sv[hf][gr];
-        if (MASK && !seen[nt][i]) wt[nt][gr][i] = 0.f;  // (a scale past the limit may be anything)
       }
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) l[nt][e] = st.l[nt][e] + (p[nt][e] + p[nt][2 + e]);
   };
+  auto times_scale = [&](int nt, int gr, int i) {  // (a scale past the limit may be anything)
+    return MASK && !seen[nt][i] ? 0.f : p[nt][i] * sv[i >> 1][gr];
+  };
+  auto weigh = [&](int nt) {
+#pragma unroll
+    for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wt[nt][gr][i] = times_scale(nt, gr, i) * st.factor[nt][gr][i & 1];
+  };
   float big = 0.f, lbig = 0.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    probabilities(nt);
     weigh(nt);
 #pragma unroll
     for (int gr = 0; gr < GR; ++gr) {
@@ -455,36 +466,43 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
   if (__any_sync(0xffffffffu, !(big <= kLimit) || !(lbig <= kMostSum))) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float f[2], rise[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float z = -INFINITY;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float big_s = fmaxf(fmaxf(sv[hf][0], sv[hf][GR - 1]), kSmall);
-          if (!MASK || seen[nt][2 * hf + e])
-            z = fmaxf(z, fmaf(dot(nt, 2 * hf + e), st.back[nt][e], __log2f(big_s)));
-        }
+        for (int hf = 0; hf < 2; ++hf)
+          if (!MASK || seen[nt][2 * hf + e]) z = fmaxf(z, dot(nt, 2 * hf + e) * st.back[nt][e]);
         z = column_max(z);
-        if (z - st.M[nt][e] > 14.9f) {
-          const float m1 = z - kHeadroom;
-          const float f = ex2(st.M[nt][e] - m1);
-          st.M[nt][e] = m1;
-          st.l[nt][e] *= f;
+        const float m0 = st.M[nt][e], m1 = z - m0 > 14.9f ? z - kHeadroom : m0;
+        f[e] = m1 > m0 ? ex2(m0 - m1) : 1.f;
+        rise[e] = m1 > m0 ? ex2(m1 - m0) : 1.f;
+        st.M[nt][e] = m1;
+        st.l[nt][e] *= f[e];
+      }
+      probabilities(nt);
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) {
-            st.pm[nt][gr][e] *= f;
-            if constexpr (!F32) {
-              st.eight[nt][gr][e] *= f;
-              st.eight[nt][gr][2 + e] *= f;
-            }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr) {
+          // What went to fp16 keeps its size as its reference moves, unless the new largest would not fit: that
+          // goes to [2^7, 2^8).
+          const float w = column_max(fmaxf(times_scale(nt, gr, e), times_scale(nt, gr, 2 + e)));
+          float to = fminf(st.factor[nt][gr][e] * rise[e], kMostFactor);
+          if (w * to > kLimit) to = __uint_as_float((261u - (__float_as_uint(w) >> 23)) << 23);
+          const float times = __fdividef(f[e] * to, st.factor[nt][gr][e]);
+          st.factor[nt][gr][e] = to;
+          st.pm[nt][gr][e] *= f[e];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.o[nt][gr * 4 + i][e] *= times;
+            st.o[nt][gr * 4 + i][2 + e] *= times;
           }
-#pragma unroll
-          for (int mt = 0; mt < S::MT; ++mt) {
-            st.o[nt][mt][e] *= f;
-            st.o[nt][mt][2 + e] *= f;
+          if constexpr (!F32) {
+            st.eight[nt][gr][e] *= times;
+            st.eight[nt][gr][2 + e] *= times;
           }
         }
-      }
       weigh(nt);
     }
   }
@@ -573,11 +591,11 @@ __device__ __forceinline__ bool finish_unit(State<D, NT, F32>& st, const Kv4Attn
       st.l[nt][e] = column_sum(st.l[nt][e]);
 #pragma unroll
       for (int gr = 0; gr < S::GR; ++gr) {
-        const float c = column_sum(st.pm[nt][gr][e]);
+        const float c = column_sum(st.pm[nt][gr][e]), undo = __fdividef(1.f, st.factor[nt][gr][e]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          st.o[nt][gr * 4 + i][e] = fmaf(st.o[nt][gr * 4 + i][e], F32 ? 1.f : 16777216.f, c);         // 2^24
-          st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], F32 ? 1.f : 1048576.f, c);  // 2^20
+          st.o[nt][gr * 4 + i][e] = fmaf(st.o[nt][gr * 4 + i][e], F32 ? undo : undo * 16777216.f, c);         // 2^24
+          st.o[nt][gr * 4 + i][2 + e] = fmaf(st.o[nt][gr * 4 + i][2 + e], F32 ? undo : undo * 1048576.f, c);  // 2^20
         }
       }
       const int n = nt * 8 + 2 * t + e;

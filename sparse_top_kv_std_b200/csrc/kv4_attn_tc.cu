@@ -9,8 +9,8 @@
 // into logits and weights, multiplies them by sv_0 and sv_1 and writes 16-bit rows of the next operand.
 // (O's upper 64 rows are valid for group 0's channels, the lower for group 1's: half of the product is
 // thrown away, which costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
-// reference of each row that moves only when some weight would leave fp16's range, so a tile has one
-// barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
+// reference of each row, and their products with a group's scales have a factor of the row's and group's own; both
+// move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
 // x 4 heads x 33,024 keys, 49 rows, 368 us (four blocks of 16 rows in kv4_attn.cu: 727 us; 403 where a thread
@@ -35,8 +35,9 @@ constexpr int kStages = 4;
 constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 13;
 static_assert(kIssueS != kIssuePV && kIssueS != kFetcher / 32 && kIssuePV != kFetcher / 32, "one role a warp");
 constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
-constexpr float kSmall = 9.094947e-13f;
+constexpr float kMostFactor = 1.3292280e36f;
 constexpr float kHeadroom = 8.f;
+constexpr float kMostWeight = 1.1529215e18f;  // 2^60: a weight above it moves its reference, however small the scales
 
 // Shared memory, from a 1024-byte boundary on: operands in 128-byte swizzled rows, then the ring of 4-bit
 // tiles, then tables.
@@ -51,7 +52,7 @@ struct Lay {
   static constexpr int Q_GROUP = kRows * 128;
   static constexpr int RING = Q + GR * Q_GROUP;
   static constexpr int TAB = RING + kStages * TileAt<D>::BYTES;
-  static constexpr int RED = TAB + 6 * kRows * 4;         // [4 warps][64 rows][3]
+  static constexpr int RED = TAB + 10 * kRows * 4;        // [4 warps][64 rows][3]
   static constexpr int BYTES = RED + 4 * kRows * 3 * 4;
 };
 
@@ -249,6 +250,7 @@ __device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Unit& u
     tab[2 * kRows + r] = INFINITY;  // minus the row's reference
     reinterpret_cast<int*>(tab)[4 * kRows + r] = n0 + (row < a.rows ? row % a.nq : 0);  // keys it attends
     tab[5 * kRows + r] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+    tab[6 * kRows + r] = tab[7 * kRows + r] = kMostFactor;
   }
 }
 
@@ -290,7 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
   const int64_t begin64 = (int64_t)share * blockIdx.x;
   const int begin = begin64 < total ? (int)begin64 : total, end = min(begin + share, total);
   const uint32_t ring = sm + L::RING;
-  // of the rows: sums of q (two groups), minus the references, factors, keys they attend, powers of two
+  // Of the rows: [0], [1] sums of q (two groups), [2] minus the references, [3] what sums of weights are multiplied
+  // with when those move, [4] the keys they attend, [5] their powers of two, [6], [7] the factors of weights x
+  // scales (two groups), [8], [9] what the sums of those are multiplied with.
   float* tab = reinterpret_cast<float*>(smem + L::TAB);
   float* red = reinterpret_cast<float*>(smem + L::RED);
   if (tid == kFetcher && begin < end) {
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
       // this thread's key: scales (K's with log2(e) / sqrt(d), and 2^24 as codes are subnormals), position
       constexpr float kBack = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f) * 16777216.f;
       const int pos = (first + i) * kTile + key;
-      float sk[GR], mk[GR], sv[GR], mv[GR], smax = kSmall;
+      float sk[GR], mk[GR], sv[GR], mv[GR];
 #pragma unroll
       for (int gr = 0; gr < GR; ++gr) {
         const uint32_t uk = lds32(cur + At::KS + key * At::SW + 4 * gr), uv = lds32(cur + At::VS + key * At::SW + 4 * gr);
@@ -401,25 +405,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         mk[gr] = hi_bf16(uk) * kBack;
         sv[gr] = lo_bf16(uv);
         mv[gr] = fmaf(8.f, sv[gr], hi_bf16(uv));
-        smax = fmaxf(smax, sv[gr]);
       }
       const bool edge = (first + i + 1) * kTile > n0;  // some query position does not attend some key of the tile
       if (edge && pos >= keys) {  // (past the last key the bytes may be anything)
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) sk[gr] = mk[gr] = sv[gr] = mv[gr] = 0.f;
-        smax = kSmall;
       }
       wait_for(&ctl.s_done, (s_count - 1) & 1u, &ctl.abort, a.err);
       tc::fence_after_sync();
 
       const uint32_t s_at = lanes + C::S + (i & 1) * GR * kRows + wg * 8;
       const uint32_t p_at = sm + L::P + buf * 2 * L::P_GROUP + key * 128;
-      // Weights and the operand's rows.  Where some weight leaves fp16's range (the first tile of a unit, as
-      // no reference is set yet, and rarely after it) the references move and it is done once more; a thread
-      // whose own weights fit has added them to its sums by then, which move with the references.
+      // Weights and the operand's rows.  Where some weight x scale x factor leaves fp16's range (the first tile of a
+      // unit, as no reference is set yet, and rarely after it) references and factors move and it is done once more; a
+      // thread whose own weights fit has added them to its sums by then, which move with the references.
       bool added = false;
       for (bool moved = false;;) {
-        float big = 0.f;
+        float big = 0.f, most = 0.f;
         f32x2 p[kShare / 2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -469,17 +471,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
             for (int k = 0; k < 4; ++k) {
               float x0, x1;
               f2_split(x[k], x0, x1);
-              const f32x2 pp = f2_make(ex2(x0), ex2(x1));
-              p[4 * h + k] = pp;
-              float w0, w1;
-              f2_split(f2_mul(pp, f2_make(smax, smax)), w0, w1);
-              big = max3f(big, w0, w1);
-#pragma unroll
-              for (int gr = 0; gr < GR; ++gr) {
-                f2_split(f2_mul(pp, f2_make(sv[gr], sv[gr])), w0, w1);
-                pk[gr][k] = as_u32(__floats2half2_rn(w0, w1));
-              }
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              most = max3f(most, x0, x1);
+              p[4 * h + k] = f2_make(x0, x1);
             }
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(at + (6 + gr) * kRows + 2 * k);
+                const f32x2 s2 = f2_make(sv[gr], sv[gr]);
+                float w0, w1;
+                f2_split(f2_mul(f2_mul(p[4 * h + k], s2), f.x), w0, w1);
+                big = max3f(big, w0, w1);
+                pk[gr][k] = as_u32(__floats2half2_rn(w0, w1));
+                f2_split(f2_mul(f2_mul(p[4 * h + k + 1], s2), f.y), w0, w1);
+                big = max3f(big, w0, w1);
+                pk[gr][k + 1] = as_u32(__floats2half2_rn(w0, w1));
+              }
             const int chunk = 4 * h + wg;
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr)
@@ -489,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
             for (int k = 0; k < 4; ++k) p[4 * h + k] = 0;
           }
         }
-        const bool fits = big <= kLimit;
+        const bool fits = big <= kLimit && most <= kMostWeight;
         if (!added && (fits || moved)) {
           added = true;
           if (edge && (mv[0] != mv[0] || mv[GR - 1] != mv[GR - 1])) {
@@ -527,40 +537,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         tc::fence_after_sync();
         moved = true;
-        // every row's largest logit + log2 of the key's scale, first over the warps
-        const float ls = __log2f(smax);
+        auto each_logit = [&](auto f) {  // f(row, logit): the logits above, summed in the same order
 #pragma unroll 1
-        for (int r = 0; r < 8 * halves; r += 4) {
-          const int row0 = (r >> 3) * (kRows / 2) + wg * 8 + (r & 4);
-          uint32_t s[GR][4];
+          for (int r = 0; r < 8 * halves; r += 4) {
+            const int row0 = (r >> 3) * (kRows / 2) + wg * 8 + (r & 4);
+            uint32_t s[GR][4];
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_x4(s_at - wg * 8 + gr * kRows + row0, s[gr]);
+            for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_x4(s_at - wg * 8 + gr * kRows + row0, s[gr]);
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_wait4(s[gr]);
+            for (int gr = 0; gr < GR; ++gr) tc::tmem_ld_wait4(s[gr]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = row0 + k;
-            float x = mk[0] * tab[row];  // (the sum above, in its order)
-            if constexpr (GR == 2) x = fmaf(mk[1], tab[kRows + row], x);
+            for (int k = 0; k < 4; ++k) {
+              const int row = row0 + k;
+              float x = mk[0] * tab[row];
+              if constexpr (GR == 2) x = fmaf(mk[1], tab[kRows + row], x);
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), x);
-            x = fmaf(x, tab[5 * kRows + row], ls);
-            const float z = warp_max(pos < reinterpret_cast<const int*>(tab)[4 * kRows + row] ? x : -INFINITY);
-            if (lane == 0) red[qd * kRows + row] = z;
+              for (int gr = 0; gr < GR; ++gr) x = fmaf(sk[gr], __uint_as_float(s[gr][k]), x);
+              f(row, x, pos < reinterpret_cast<const int*>(tab)[4 * kRows + row]);
+            }
           }
-        }
+        };
+        auto over_warps = [&](int i) {
+          return fmaxf(fmaxf(red[i], red[2 * kRows + i]), fmaxf(red[4 * kRows + i], red[6 * kRows + i]));
+        };
+        const bool mine = tid < kRows && (tid & ~7) < live;  // (rows behind the last share its eight)
+        // every row's largest logit, first over the warps
+        each_logit([&](int row, float x, bool seen) {
+          const float z = warp_max(seen ? x * tab[5 * kRows + row] : -INFINITY);
+          if (lane == 0) red[2 * (qd * kRows + row)] = z;
+        });
         __syncthreads();
         if (tid < kRows) {
-          float f = 1.f;
-          if ((tid & ~7) < live) {  // (rows behind the last share its eight)
-            const float z = fmaxf(fmaxf(red[tid], red[kRows + tid]), fmaxf(red[2 * kRows + tid], red[3 * kRows + tid]));
-            const float m0 = -tab[2 * kRows + tid];
-            if (z - m0 > 14.9f) {
-              f = ex2(m0 - (z - kHeadroom));
-              tab[2 * kRows + tid] = kHeadroom - z;
+          float f = 1.f, times[2] = {1.f, 1.f};
+          const float m0 = -tab[2 * kRows + tid], z = mine ? over_warps(2 * tid) : m0;
+          if (z - m0 > 14.9f) {
+            const float m1 = z - kHeadroom, rise = ex2(m1 - m0);
+            f = ex2(m0 - m1);
+            tab[2 * kRows + tid] = -m1;
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr) {  // (what went to fp16 keeps its size)
+              const float f0 = tab[(6 + gr) * kRows + tid], f1 = fminf(f0 * rise, kMostFactor);
+              tab[(6 + gr) * kRows + tid] = f1;
+              times[gr] = __fdividef(f * f1, f0);
             }
           }
           tab[3 * kRows + tid] = f;
+          tab[8 * kRows + tid] = times[0];
+          tab[9 * kRows + tid] = times[1];
+        }
+        __syncthreads();
+        // every row's largest weight x scale in each group
+        each_logit([&](int row, float x, bool seen) {
+          const float w = seen ? ex2(fmaf(x, tab[5 * kRows + row], tab[2 * kRows + row])) : 0.f;
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) {
+            const float top = warp_max(seen ? w * sv[gr] : 0.f);
+            if (lane == 0) red[2 * (qd * kRows + row) + gr] = top;
+          }
+        });
+        __syncthreads();
+        if (mine) {
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr) {
+            const float w = over_warps(2 * tid + gr), f0 = tab[(6 + gr) * kRows + tid];
+            if (w * f0 > kLimit) {  // to [2^7, 2^8)
+              const float f1 = __uint_as_float((261u - (__float_as_uint(w) >> 23)) << 23);
+              tab[(6 + gr) * kRows + tid] = f1;
+              tab[(8 + gr) * kRows + tid] *= __fdividef(f1, f0);
+            }
+          }
         }
         __syncthreads();
         const f32x2* f = reinterpret_cast<const f32x2*>(tab + 3 * kRows + wg * 8);
@@ -573,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         }
         if (pv_count > pv0) {
           // this thread's row (lane) of O, a quarter of its group's channels
-          const float fr = tab[3 * kRows + (key & 63)];
+          const float fr = tab[(8 + (key >> 6)) * kRows + (key & 63)];
           if (GR == 2 || key < 64) {
             const uint32_t o_at = lanes + C::O + (key < 64 ? 0 : 64) + wg * 16;
             uint32_t o[16];
@@ -664,9 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           sp += red[(w * kRows + row) * 3 + 1 + gr];
         }
         const float inv = sl == 0.f ? 0.f : 1.f / sl;  // a row that attends no key: zeros
+        const float undo = __fdividef(1.f, tab[(6 + gr) * kRows + row]);
         float v[16];  // in the channels' order
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[(j & 8) + perm8(j & 7)] = __uint_as_float(o[j]) + sp;
+        for (int j = 0; j < 16; ++j) v[(j & 8) + perm8(j & 7)] = fmaf(__uint_as_float(o[j]), undo, sp);
         if (whole) {
           const int64_t at = ((((int64_t)u.l * a.B + u.b) * a.Hq + u.h * a.G) * a.nq + r) * D + c0;
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at;

@@ -196,3 +196,70 @@ def test_constant_values_with_rising_logits(dtype, d, G, rows, power):
     q = sign.expand(L, 1, G * Hkv, rows, d)
     o, q, c = _attend(q.contiguous(), k.contiguous(), v.contiguous(), rows, [n], dtype)
     _check(o, q, c, [n], dtype)
+
+
+# ----------------------------------------------------------------------------- groups of values
+
+def _groups(kind, L, nB, Hkv, cap, d, seed):
+    """Values and the powers of two of their groups, [..., cap][d / 64]."""
+    v = _randn(seed, L, nB, Hkv, cap, d)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    e = torch.zeros(L, nB, Hkv, cap, d // 64, device="cuda")
+    if kind == "keys":        # every key and group of a size of its own
+        e = torch.randint(-30, 31, e.shape, generator=g, device="cuda").float()
+    elif kind == "steps":     # sizes rise and fall with the tiles, in opposite directions
+        t = torch.arange(cap, device="cuda") // 128
+        e[..., 0] = 12.0 * (t * 3 % 5 - 2)
+        e[..., -1] -= 9.0 * (t * 2 % 7 - 3)
+    elif kind == "tiny":
+        e -= 80
+    elif kind == "large":
+        e += 37
+    else:                     # the second group 2^kind of the first
+        e[..., 1] = kind
+    return (v.view(*e.shape, 64) * torch.exp2(e)[..., None]).view(v.shape)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("G,rows", HEADS)
+@pytest.mark.parametrize("kind", [-12, -16, -24, -40, 24, "keys", "tiny", "large"])
+def test_value_groups_of_different_sizes(dtype, G, rows, kind):
+    lens = [1100, 77]
+    q = _randn(9, 1, 2, 2 * G, rows, 128)
+    k, v = _randn(10, 1, 2, 2, 1136, 128), _groups(kind, 1, 2, 2, 1136, 128, 11)
+    o, q, c = _attend(q, k, v, rows, lens, dtype)
+    _check(o, q, c, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,rows", HEADS[:3])
+@pytest.mark.parametrize("height", [0, 7, 45])
+def test_sizes_and_logits_that_move_from_tile_to_tile(dtype, d, G, rows, height):
+    """Several tiles a CTA: references and the groups' factors move, up and down, while sums are under way."""
+    L, Hkv, n = 6, 8, 2000
+    sign = torch.sign(_randn(12, d))
+    cap = n + 16 + rows // 16 * 16
+    k = _steps(sign, cap, d, height) + 0.3 * _randn(13, L, 1, Hkv, cap, d)
+    q = sign + 0.3 * _randn(14, L, 1, G * Hkv, rows, d)
+    v = _groups("steps", L, 1, Hkv, cap, d, 15)
+    o, q, c = _attend(q, k, v, rows, [n], dtype)
+    _check(o, q, c, [n], dtype)
+
+
+@pytest.mark.parametrize("d,G,rows", [(128, 1, 1), (128, 5, 3)])
+@pytest.mark.parametrize("kind", [-12, -16, -24])
+def test_fp32_accuracy_in_both_groups(d, G, rows, kind):
+    """Diffuse attention, the result a small difference of large sums: a fp32 accumulator of centred codes is off by
+    sqrt(n / 128) 2^-23 of the result, 5e-7 here, the logits' own rounding (2^-22 of some 30 in each) as much
+    as four times that, at random: 8e-6 in norm, in either group."""
+    n = 2112
+    q, k = _randn(16, 1, 1, G, rows, d), _randn(17, 1, 1, 1, n + 16, d)
+    o, q, c = _attend(q, k, _groups(kind, 1, 1, 1, n + 16, d, 18), rows, [n], torch.float32)
+    for at, Q, keys, K, V in _units(q, c, [n]):
+        x, _ = _logits(Q, keys, K)
+        p = np.exp(x - x.max(1, keepdims=True))
+        want = p @ (V[2] + V[0] * V[1]) / p.sum(1, keepdims=True)
+        got = o[at].reshape(want.shape)
+        for g in (slice(0, 64), slice(64, 128)):
+            assert np.linalg.norm((got - want)[:, g]) <= 8e-6 * np.linalg.norm(want[:, g])
