@@ -263,3 +263,21 @@ def test_fp32_accuracy_in_both_groups(d, G, rows, kind):
         got = o[at].reshape(want.shape)
         for g in (slice(0, 64), slice(64, 128)):
             assert np.linalg.norm((got - want)[:, g]) <= 8e-6 * np.linalg.norm(want[:, g])
+
+
+# ----------------------------------------------------------------------------- large logits
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,rows", HEADS)
+@pytest.mark.parametrize("power", [24, 40, 100])
+@pytest.mark.parametrize("value_power", [0, 39])
+def test_logits_whose_rounding_exceeds_the_exponents(dtype, d, G, rows, power, value_power):
+    """Logits far above 2^24, where one unit in the last place is many powers of two: the weights and the reference
+    that they are relative to round alike, so the largest logit's weight is finite and not zero."""
+    lens = [900, 40]
+    q = _randn(19, 1, 2, 2 * G, rows, d) * 2.0 ** power
+    k, v = _randn(20, 1, 2, 2, 944, d), _randn(21, 1, 2, 2, 944, d) * 2.0 ** value_power
+    o, q, c = _attend(q, k, v, rows, lens, dtype)
+    assert np.isfinite(o).all()
+    assert _check_largest_logit(o, q, c, lens, dtype) > 0
