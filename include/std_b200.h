@@ -496,6 +496,7 @@ int std_accept_prefix(int B, int gamma, const int32_t* draft, const int32_t* den
 /* The rotation.  The first rot_dim channels of a head are rot_dim / 2 pairs; pair i is channels
  * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when `interleaved`, and turns by
  * t = position * inv_freq[i]:  (a, b) -> (a cos t - b sin t, b cos t + a sin t).
+ * The other channels are not rotated: without a norm they pass through, whatever they hold.
  * A video's tokens may have a position on up to three axes (frame, row, column): the first
  * section[0] pairs turn with axis 0, the next section[1] with axis 1, the others with axis 2. */
 typedef struct std_rope {

@@ -101,15 +101,17 @@ __device__ __forceinline__ void load_heads(Vec<E * sizeof(T)> (&v)[kBatch], cons
 
 // The heads of one part, the first kBatch of them loaded.  Channel j of a lane becomes
 //   x_j (c_j w_j) inv + x_partner (s_j w_partner) inv
-// so the weights join the cosines and signed sines (c = 1, s = 0 past the rotated channels), once for
-// all heads, and the partner's value travels as it was read, two bf16 in a shuffle.
-template <typename T, int E, bool ROTATE>
+// so the weights join the cosines and signed sines, once for all heads, and the partner's value travels as it
+// was read, two bf16 in a shuffle.  Past the rotated channels (of which ALL has none: 2 us of the prompt below) c
+// is 1 and the second product left out, whatever it is.
+template <typename T, int E, bool ROTATE, bool ALL>
 __device__ __forceinline__ void run_heads(Vec<E * sizeof(T)> (&v)[kBatch], const Part<T>& p, const float2* cs, int half,
                                           bool interleaved, float eps, int e0, uint32_t mask) {
   constexpr int D = 16 * E;
   using V = Vec<E * sizeof(T)>;
   float c[E], s[E];
   int partner = threadIdx.x & 31;
+  const bool past = !ALL && e0 >= 2 * half;
   if constexpr (ROTATE) {
     // (E divides half, so a lane lies wholly in the first half, the second, or past both)
     const bool first = e0 < half, second = !first && e0 < 2 * half;
@@ -162,7 +164,7 @@ __device__ __forceinline__ void run_heads(Vec<E * sizeof(T)> (&v)[kBatch], const
           inv = rsqrtf(ss * (1.f / D) + eps);
         }
 #pragma unroll
-        for (int j = 0; j < E; ++j) x[j] = (x[j] * c[j] + y[j] * s[j]) * inv;
+        for (int j = 0; j < E; ++j) x[j] = (x[j] * c[j] + (past ? -0.f : y[j] * s[j])) * inv;
         pack<T, E>(x, v[i]);
       }
       v[i].store(p.dst + (h + i) * p.dst_step + e0);
@@ -268,12 +270,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && TOK > 1 ? 3 : 1) q
     const Part<T> p = part_of(which);
     if (p.n <= 0) continue;
     if (which != start) load_heads<T, E>(x, p, 0, e0);
-    run_heads<T, E, true>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
+    if (a.rot_dim == D)
+      run_heads<T, E, true, true>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
+    else
+      run_heads<T, E, true, false>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
   }
   const Part<T> p = part_of(2);
   if (p.n > 0) {  // (values are copied bit for bit)
     if (start != 2) load_heads<T, E>(x, p, 0, e0);
-    run_heads<T, E, false>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
+    run_heads<T, E, false, true>(x, p, cs[t], half, a.interleaved, a.eps, e0, mask);
   }
 }
 

@@ -1,0 +1,62 @@
+"""std_qk_norm_rope where the tests of its values do not reach: channels that are not rotated."""
+import pytest
+import torch
+
+from sparse_top_kv_std_b200 import binding as B
+from tests.test_gpu_rope import _check, _make, _run
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    B.lib()
+    B.std_get_device_error(clear=True)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (32, torch.float32), (96, torch.float32)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rotated", [0, 0.5])
+@pytest.mark.parametrize("rows", [1, 9])
+def test_channels_past_the_rotated_ones_pass_through(d, dtype, interleaved, rotated, rows):
+    """Without a norm they are copied, whatever they hold; with one, an infinity makes the others of its head 0
+    and itself NaN (x / infinity)."""
+    rot = int(d * rotated)
+    for norm in (False, True):
+        c = _make(1, 1, rows, 4, 2, d, dtype, [3], rot, 1, 1, fused=False, norm=norm, interleaved=interleaved)
+        plain = _run(c)
+        c["q"][0, 0, 0, 1, rot + 2] = INF
+        c["q"][0, 0, 0, 2, rot + 5] = -INF
+        c["q"][0, 0, 0, 3, d - 1] = float("nan")
+        c["k"][0, 0, 0, 1, d - 2] = INF
+        q, k, v, cv = _run(c)
+        cv.check()
+        if norm:
+            for head, ch in ((q[0, 0, 1, 0], rot + 2), (q[0, 0, 2, 0], rot + 5), (k[0, 0, 1, 3], d - 2)):
+                others = torch.arange(d, device="cuda") != ch
+                assert torch.isnan(head[ch]) and (head[others] == 0).all()
+            assert torch.isnan(q[0, 0, 3, 0]).all()
+        else:
+            for got, want in ((q[0, 0], c["q"][0, 0].transpose(0, 1)), (k[0, 0, :, 3:3 + rows], c["k"][0, 0].transpose(0, 1))):
+                a, b = got[..., rot:], want[..., rot:]
+                bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+                assert torch.equal(torch.isnan(a), torch.isnan(b))
+                assert torch.equal(torch.nan_to_num(a).view(bits), torch.nan_to_num(b).contiguous().view(bits))
+                assert torch.isfinite(got[..., :rot]).all()
+        # the rotated channels of heads without one, and all other heads, are as before
+        assert torch.equal(q[0, 0, 0], plain[0][0, 0, 0]) and torch.equal(k[0, 0, 0], plain[1][0, 0, 0])
+        if not norm:
+            assert torch.equal(q[..., :rot], plain[0][..., :rot]) and torch.equal(k[..., :rot], plain[1][..., :rot])
+    assert B.std_get_device_error() == 0
+
+
+def test_zeros_keep_their_signs_without_norm_and_rotation():
+    c = _make(1, 1, 5, 4, 2, 64, torch.float32, [0], 0, 1, 2, norm=False, fused=False)
+    c["q"][..., ::3] = -0.0
+    q, _, _, cv = _run(c)
+    cv.check()
+    assert torch.equal(q[0, 0].view(torch.int32), c["q"][0, 0].transpose(0, 1).contiguous().view(torch.int32))
