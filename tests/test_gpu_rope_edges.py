@@ -1,4 +1,4 @@
-"""std_qk_norm_rope where the tests of its values do not reach: channels that are not rotated."""
+"""std_qk_norm_rope where the tests of its values do not reach: channels that are not rotated, and every grid of its launch."""
 import pytest
 import torch
 
@@ -60,3 +60,51 @@ def test_zeros_keep_their_signs_without_norm_and_rotation():
     q, _, _, cv = _run(c)
     cv.check()
     assert torch.equal(q[0, 0].view(torch.int32), c["q"][0, 0].transpose(0, 1).contiguous().view(torch.int32))
+
+
+# ----------------------------------------------------------------------------- grids
+
+def _grid(tokens, rows, heads, sms):
+    """Tokens of a CTA and whether sequences share CTAs, by the launch's rule."""
+    most = sms * (12 if heads > 16 else 6) // 5
+    parts = -(-heads // 16)
+    if tokens * parts <= most:
+        return 1, False
+    tok = next((t for t in (2, 4, 8) if tokens <= t * most), 16)
+    places = -(-rows // tok) * tok
+    return tok, 10 * (places - rows) > places
+
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(torch.bfloat16, 128, 14, 2), (torch.bfloat16, 64, 6, 1), (torch.float32, 64, 4, 2)])
+@pytest.mark.parametrize("tok", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("axes", [1, 3])
+def test_every_number_of_tokens_a_cta(dtype, d, Hq, Hkv, tok, shared, axes):
+    """Chunks of a sequence's own with a remainder, and CTAs shared by sequences, of 1 to 16 tokens: padded
+    batches, as many tokens as the rule of the launch asks for on this device."""
+    if tok == 1 and shared:
+        pytest.skip("a CTA of one token is not shared")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    heads = Hq + 2 * Hkv
+    most = sms * (12 if heads > 16 else 6) // 5
+    if tok == 1:
+        nB, rows = 3, most // -(-heads // 16) // 3
+    elif shared:
+        rows = {2: 3, 4: 5, 8: 11, 16: 19}[tok]
+        nB = (most * tok * 3 // 4) // rows if tok < 16 else most * 9 // rows
+    else:
+        nB = 2
+        rows = (most * tok * 3 // 4 if tok < 16 else most * 9) // nB | 1
+    assert _grid(nB * rows, rows, heads, sms) == (tok, shared)
+    n = [rows, rows - 1] + [(7 * b) % (rows + 1) for b in range(2, nB)]
+    if not shared:
+        n[-1] = rows // 2 // tok * tok + 1       # one token in its last chunk
+    lens = [(5 * b) % 11 for b in range(nB)]
+    c = _make(1, nB, rows, Hq, Hkv, d, dtype, lens, d, axes, 3, ragged=n)
+    for b in range(nB):
+        for x in "qkv":
+            c[x][:, b, n[b]:] = float("nan")     # never read
+    q, k, v, cv = _run(c)
+    cv.check()
+    assert B.std_get_device_error() == 0
+    _check(c, q, k, v)
