@@ -60,7 +60,8 @@ class Kv4Session:
         B_.std_kv4_quantize(self.dims, self.cache4, self.k_full, self.v_full, None, self.len_full, self.dims.cap_full)
 
     def round(self, io: Dict[str, torch.Tensor]) -> None:
-        """io: the tensors of a std_round_io (round_outputs() makes its outputs)."""
+        """io: the tensors of a std_round_io (round_outputs() makes its outputs).  A sequence without room for
+        gamma + 1 rows is flagged (STD_DEVERR_*) and its context left as it is."""
         d, g = self.dims, self.gamma
         for j in range(g):
             B_.std_kv4_append(d, self.cache4, self.len_full, j, io["k_draft"][j], io["v_draft"][j], 1)
@@ -68,9 +69,12 @@ class Kv4Session:
         B_.std_dense_verify_attn_append(d, io["q_verify"], g, self.k_full, self.v_full, self.len_full, io["k_verify"],
                                         io["v_verify"], io["o_verify"], 0, self.ws)
         B_.std_accept_prefix(self.B, g, io["draft_tokens"], io["dense_tokens"], io["n_plus_1"], io["accepted"])
-        # the accepted inputs' rows replace the draft's own; what lies behind them is not read again
-        B_.std_kv4_quantize(d, self.cache4, self.k_full, self.v_full, self.len_full, io["n_plus_1"], g + 1)
-        self.len_full += io["n_plus_1"]
+        # the accepted inputs' rows replace the draft's own; what lies behind them is not read again.  The verify
+        # has appended nothing to a sequence whose rows would pass the capacity: none of them are accepted.
+        fits = (self.len_full >= 0) & (self.len_full <= d.cap_full - (g + 1))
+        n = io["n_plus_1"] * fits
+        B_.std_kv4_quantize(d, self.cache4, self.k_full, self.v_full, self.len_full, n, g + 1)
+        self.len_full += n
 
     def round_outputs(self) -> Dict[str, torch.Tensor]:
         """o_draft (in the queries' type), o_verify, n_plus_1 and accepted of one round."""
