@@ -12,6 +12,7 @@ the output is that of dense decoding:
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Dict
 
 import torch
@@ -41,6 +42,14 @@ class Kv4Cache(dict):
         return sum(t.numel() * t.element_size() for t in self.values() if torch.is_tensor(t))
 
 
+def _on(stream):
+    """The context in which torch and the library work on `stream` (a torch stream, a handle, or None: the
+    current one)."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class Kv4Session:
     def __init__(self, L: int, B: int, Hq: int, Hkv: int, d: int, dtype: int, cap: int, gamma: int, device="cuda"):
         self.L, self.B, self.Hq, self.Hkv, self.d, self.gamma = L, B, Hq, Hkv, d, gamma
@@ -54,14 +63,19 @@ class Kv4Session:
                    B_.std_attn_workspace_size(self.dims, gamma + 1, cap, 0))
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
 
-    def start(self, n) -> None:
+    def start(self, n, stream=None) -> None:
         """Set the committed lengths (n: one for each sequence) and copy their rows to the 4-bit cache."""
-        self.len_full.copy_(torch.as_tensor(n, dtype=torch.int32))
-        B_.std_kv4_quantize(self.dims, self.cache4, self.k_full, self.v_full, None, self.len_full, self.dims.cap_full)
+        with _on(stream):
+            self.len_full.copy_(torch.as_tensor(n, dtype=torch.int32))
+            B_.std_kv4_quantize(self.dims, self.cache4, self.k_full, self.v_full, None, self.len_full, self.dims.cap_full)
 
-    def round(self, io: Dict[str, torch.Tensor]) -> None:
+    def round(self, io: Dict[str, torch.Tensor], stream=None) -> None:
         """io: the tensors of a std_round_io (round_outputs() makes its outputs).  A sequence without room for
         gamma + 1 rows is flagged (STD_DEVERR_*) and its context left as it is."""
+        with _on(stream):
+            self._round(io)
+
+    def _round(self, io) -> None:
         d, g = self.dims, self.gamma
         for j in range(g):
             B_.std_kv4_append(d, self.cache4, self.len_full, j, io["k_draft"][j], io["v_draft"][j], 1)

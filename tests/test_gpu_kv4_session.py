@@ -1,4 +1,4 @@
-"""Kv4Session at a cache's end."""
+"""Kv4Session at a cache's end, on streams and in graphs."""
 import pytest
 import torch
 
@@ -22,11 +22,12 @@ def _randn(seed, *shape):
     return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").bfloat16()
 
 
-def _session(n):
+def _session(n, stream=None):
     s = Kv4Session(L, NB, HQ, HKV, D, B.STD_BF16, CAP, GAMMA)
     s.k_full.copy_(_randn(1, *s.k_full.shape))
     s.v_full.copy_(_randn(2, *s.v_full.shape))
-    s.start(n)
+    torch.cuda.synchronize()
+    s.start(n, stream=stream)
     return s
 
 
@@ -79,3 +80,44 @@ def test_a_round_that_just_fits_is_accepted():
     torch.cuda.synchronize()
     assert B.std_get_device_error(clear=True) == 0
     assert s.len_full.tolist() == [CAP, 6, 5]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_rounds_on_another_stream_and_in_a_graph(handle):
+    lens, accepted = [100, 61, 0], [2, 4, 0]
+    s = _session(lens)
+    want = _io(s, 10, accepted)
+    s.round(want)
+    torch.cuda.synchronize()
+    want4 = _copy4(s)
+
+    side = torch.cuda.Stream()
+    t = _session(lens, stream=side.cuda_stream if handle else side)
+    got = _io(t, 10, accepted)
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(side):
+        for _ in range(20):                      # the round has to wait for its own stream, not for the current one
+            busy.add_(1)
+    t.round(got, stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    assert t.len_full.tolist() == s.len_full.tolist()
+    for x in ("o_draft", "o_verify", "n_plus_1", "accepted"):
+        assert torch.equal(got[x], want[x])
+    assert all(torch.equal(a, b) for a, b in zip(_copy4(t), want4))
+
+    u = _session(lens)
+    io = _io(u, 10, accepted)
+    graph = torch.cuda.CUDAGraph()
+    u.round(io)                                  # (first calls set kernels up)
+    u.start(lens)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        u.round(io)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert u.len_full.tolist() == s.len_full.tolist()
+    for x in ("o_draft", "o_verify", "n_plus_1", "accepted"):
+        assert torch.equal(io[x], want[x])
+    assert all(torch.equal(a, b) for a, b in zip(_copy4(u), want4))
+    assert B.std_get_device_error(clear=True) == 0
