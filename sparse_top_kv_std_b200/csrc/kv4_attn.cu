@@ -35,8 +35,6 @@
 // of the integer pipe are used: four warps a scheduler do not hide their own latencies.
 #include "kv4_attn.cuh"
 
-#include <cuda_fp16.h>
-
 #include <atomic>
 #include <type_traits>
 
@@ -45,20 +43,15 @@ namespace {
 
 constexpr int kWarps = kTile / 16;       // warps that compute, 16 keys each
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLimit = 32768.f;        // largest weight x scale x factor that goes to fp16
-constexpr float kMostFactor = 1.3292280e36f;  // 2^120: a factor of weights x scales before any was seen
 // 2^70: a sum of weights above it moves the reference too, where scales are so small (0, for constant values) that
 // weight x scale never does.  Minima are below 2^41 in magnitude (values up to 2^40), so that sum p (mv + 8 sv) of a
 // lane stays below 2^111, and of all warps and CTAs below 2^122.
 constexpr float kMostSum = 1.1805916e21f;
-constexpr float kHeadroom = 8.f;         // a new reference puts the largest weight at 2^8
 
 // ---------------------------------------------------------------- shared memory
 template <int D, int NT, bool F32>
 struct Layout {
-  static constexpr int CW = D / 2;                      // code bytes of a row
-  static constexpr int SW = D / kKv4Group * 4;          // scale bytes of a row
-  static constexpr int STAGE = 2 * kTile * (CW + SW);   // K codes, V codes, K scales, V scales
+  static constexpr int CW = TileAt<D>::CW, SW = TileAt<D>::SW, STAGE = TileAt<D>::BYTES;
   static constexpr int ROWS = 8 * NT;
   static constexpr int OSTR = D + 4;                    // row stride of the merge buffer, floats
   static constexpr int MERGE = kWarps * ROWS * OSTR * 4;
@@ -98,33 +91,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // 16-bit elemen
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-
-// Two codes as fp16 subnormals: c 2^-24 from bits 0-3 and 16-19, c 2^-20 from bits 4-7 and 20-23.
-__device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
-// Two codes as c - 8, one instruction more: 0x6400 is 1024, whose last ten bits hold a code at bit 0 or 4.
-__device__ __forceinline__ uint32_t centre0(uint32_t w) {
-  return as_u32(__hsub2(as_h2(widen0(w) | 0x64006400u), __float2half2_rn(1032.f)));
-}
-__device__ __forceinline__ uint32_t centre4(uint32_t w) {
-  return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
-}
 constexpr uint32_t kEight0 = 0x00080008u, kEight4 = 0x00800080u;  // the code 8 in either place
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
@@ -314,8 +284,8 @@ struct LaneAt {
     const int g = lane >> 2, t = lane & 3;
     const int kap = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);
     k = (16 * warp + kap) * Lay::CW + t * (Lay::CW / 4);
-    v = kTile * Lay::CW + (16 * warp + t) * Lay::CW + g * (Lay::CW / 8);
-    scale = 2 * kTile * Lay::CW + (lane < 16 ? 0 : kTile * Lay::SW) + (16 * warp + (lane & 15)) * Lay::SW;
+    v = TileAt<D>::VC + (16 * warp + t) * Lay::CW + g * (Lay::CW / 8);
+    scale = (lane < 16 ? TileAt<D>::KS : TileAt<D>::VS) + (16 * warp + (lane & 15)) * Lay::SW;
     w16 = Lay::AT_MERGE + warp * 512 + lane * (2 * Lay::SW);
     r16 = Lay::AT_MERGE + warp * 512 + kap * (2 * Lay::SW);
   }

@@ -2,6 +2,8 @@
 // layout of their partial results and the kernel that merges those.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -11,6 +13,33 @@ namespace stdb {
 namespace {
 
 constexpr int kTile = 128;  // keys of a tile
+constexpr float kLimit = 32768.f;  // largest weight x scale x factor that goes to fp16
+constexpr float kMostFactor = 1.3292280e36f;  // 2^120: a factor of weights x scales before any was seen
+constexpr float kHeadroom = 8.f;  // a new reference puts the largest weight at 2^8
+
+// ---------------------------------------------------------------- codes in the tensor cores
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+// Two codes as fp16 subnormals: c 2^-24 from bits 0-3 and 16-19, c 2^-20 from bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
+// Two codes as c - 8, one instruction more: 0x6400 is 1024, whose last ten bits hold a code at bit 0 or 4.
+__device__ __forceinline__ uint32_t centre0(uint32_t w) {
+  return as_u32(__hsub2(as_h2(widen0(w) | 0x64006400u), __float2half2_rn(1032.f)));
+}
+__device__ __forceinline__ uint32_t centre4(uint32_t w) {
+  return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
 
 // ---------------------------------------------------------------- work split
 // Units are numbered (layer, sequence, KV head, row block).  A unit's tiles are cut into groups of

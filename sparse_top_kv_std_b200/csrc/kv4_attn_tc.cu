@@ -17,8 +17,6 @@
 // widens a group of its key of K and not half a row, which reads all codes twice).  Of a tile's 3,350 clocks the tensor cores are busy 800; the phases follow each other.
 #include "kv4_attn.cuh"
 
-#include <cuda_fp16.h>
-
 #include <atomic>
 
 namespace stdb {
@@ -34,9 +32,6 @@ constexpr int kStages = 4;
 // where this is 368.)
 constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 13;
 static_assert(kIssueS != kIssuePV && kIssueS != kFetcher / 32 && kIssuePV != kFetcher / 32, "one role a warp");
-constexpr float kLimit = 32768.f;        // as in kv4_attn.cu
-constexpr float kMostFactor = 1.3292280e36f;
-constexpr float kHeadroom = 8.f;
 constexpr float kMostWeight = 1.1529215e18f;  // 2^60: a weight above it moves its reference, however small the scales
 
 // Shared memory, from a 1024-byte boundary on: operands in 128-byte swizzled rows, then the ring of 4-bit
@@ -78,28 +73,6 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-// two codes as fp16 subnormals, c 2^-24 and c 2^-20 (kv4_attn.cu)
-__device__ __forceinline__ uint32_t widen0(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t widen4(uint32_t w) { return w & 0x00f000f0u; }
-// two codes as c - 8: 0x6400 is 1024, whose last ten bits hold a code at bit 0 or bit 4
-__device__ __forceinline__ uint32_t centre0(uint32_t w) {
-  return as_u32(__hsub2(as_h2(widen0(w) | 0x64006400u), __float2half2_rn(1032.f)));
-}
-__device__ __forceinline__ uint32_t centre4(uint32_t w) {
-  return as_u32(__hfma2(as_h2(widen4(w) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)));
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
