@@ -511,7 +511,8 @@ typedef struct std_rope {
  *   q_out row  <- rotate(norm(q_in, q_weight[l]))
  *   cache row len[b] + pos_offset + r of k_cache <- rotate(norm(k_in, k_weight[l])), of v_cache <- v_in
  *   norm(x, w)_i = w_i x_i / sqrt(mean_j x_j^2 + eps)
- * Norm, angles (64-bit) and rotation are rounded once, to the output type.
+ * Norm, angles (64-bit) and rotation are rounded once, to the output type.  Sums of squares are float32: with a
+ * norm, entries may be up to 2^60 in magnitude.
  * q_in      [L][B][rows][Hq][d], k_in and v_in [L][B][rows][Hkv][d], of dims->dtype; neighbouring
  *           tokens are q_stride / k_stride / v_stride ELEMENTS apart (so a fused projection's
  *           output serves: stride (Hq + 2 Hkv) d), at least heads * d and a multiple of 16 bytes.
@@ -541,8 +542,8 @@ int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_i
  * A row is d / 64 groups of 64 channels (d = 64 or 128), each with a bfloat16 scale s and minimum m:
  *   m = bf16(min x),  s = bf16(max(float(max x - m), 0) / 15),  c = clamp(round(float(x - m) / s), 0, 15)
  * (ties to even; the quotient is rounded as if it were exact), and code c stands for m + c s.  A group
- * with an infinity or a NaN, or wider than fp32 can hold, reads back as NaN in all its channels; one
- * whose s is 0 reads back as m.
+ * with an infinity or a NaN, wider than fp32 can hold, or with a minimum beyond bfloat16's largest number, reads
+ * back as NaN in all its channels; one whose s is 0 reads back as m.
  *   codes   [L][B][Hkv][cap][d / 2] bytes: 32-bit words of 8 channels, channel 8 j + n of a group in
  *           bits [4 n, 4 n + 4) of its word j; at d = 128 word 2 j of a row is group 0's word j, word
  *           2 j + 1 group 1's

@@ -13,6 +13,7 @@
 
 #include "../../include/std_b200.h"
 #include "internal.h"
+#include "kv4.cuh"
 
 namespace {
 
@@ -892,6 +893,12 @@ int std_qk_norm_rope(const std_dims* dims, const std_rope* rope, const void* q_i
 
 namespace {
 
+int check_kv4_cap(int64_t cap) {
+  if (cap < 1 || cap > INT32_MAX || cap % stdb::kKv4Rows)
+    return fail(STD_ERR_INVALID_ARG, "cap = %lld must be a positive multiple of %d", (long long)cap, stdb::kKv4Rows);
+  return STD_OK;
+}
+
 int check_kv4(const std_dims* dims, const std_kv4_cache* c) {
   STD_TRY(check_dims(dims));
   if (!c) return fail(STD_ERR_INVALID_ARG, "cache is NULL");
@@ -900,9 +907,7 @@ int check_kv4(const std_dims* dims, const std_kv4_cache* c) {
   STD_TRY(check_ptr(c->k_scales, 16, "k_scales"));
   STD_TRY(check_ptr(c->v_codes, 16, "v_codes"));
   STD_TRY(check_ptr(c->v_scales, 16, "v_scales"));
-  if (c->cap < 16 || c->cap > INT32_MAX || c->cap % 16)
-    return fail(STD_ERR_INVALID_ARG, "cap = %lld must be a positive multiple of 16", (long long)c->cap);
-  return STD_OK;
+  return check_kv4_cap(c->cap);
 }
 
 int run_kv4(const std_dims* dims, const std_kv4_cache* c, const void* k, const void* v, int64_t rows_cap, int at_pos,
@@ -937,8 +942,7 @@ int plan_kv4(const std_dims* dims, int q_rows, int64_t cap, stdb::Kv4AttnArgs* a
   if (dims->B > stdb::kKv4AttnMaxB)
     return fail(STD_ERR_UNSUPPORTED, "4-bit attention: %d sequences (at most %d)", dims->B, stdb::kKv4AttnMaxB);
   if (q_rows < 1 || q_rows > 32) return fail(STD_ERR_INVALID_ARG, "q_rows = %d must be in [1, 32]", q_rows);
-  if (cap < 16 || cap > INT32_MAX || cap % 16)
-    return fail(STD_ERR_INVALID_ARG, "cap = %lld must be a positive multiple of 16", (long long)cap);
+  STD_TRY(check_kv4_cap(cap));
   *a = stdb::Kv4AttnArgs{};
   a->L = dims->L; a->B = dims->B; a->Hq = dims->Hq; a->Hkv = dims->Hkv; a->G = dims->Hq / dims->Hkv; a->nq = q_rows;
   a->rows = a->G * q_rows; a->d = dims->d; a->dtype = dims->dtype; a->cap = cap;

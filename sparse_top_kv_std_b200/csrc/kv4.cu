@@ -69,7 +69,8 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 }
 
 // Codes of 8 channels, as one word, two channels an instruction: d = fl32(x - m), q = d / s, and 1.5 2^23 added
-// to q leaves its nearest integer, ties to even, in the last bits.  That is the exact quotient's rounding:
+// to q leaves its nearest integer, ties to even, in the last bits.  That is the exact quotient's rounding (a
+// product by the reciprocal and one correction by its remainder, after Markstein, 1990):
 // q0 = d (1 / s) is off by some units in the last place, its remainder d - q0 s is exact (s has 8 bits), and
 // q0 + remainder (1 / s) rounds to the quotient to nearest.  An exact tie T = k + 1/2 comes out as T (d = T s
 // has 13 bits).  A d next to T s is at least a unit in the last place off, so q is off by more than
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) kv4_write_ke
     const bool finite = fabsf(range) <= 3.402823466e38f;  // false for a NaN or an infinity
     uint32_t w0 = 0, w1 = 0;
     if (finite && s > 0.f) {
-constexpr bool CLAMP = sizeof(T) == 4;  // (bf16: m is the smallest x)
+      constexpr bool CLAMP = sizeof(T) == 4;  // (bf16: m is the smallest x)
       if (s >= 7.888609052e-31f) {  // 2^-100
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));

@@ -10,7 +10,7 @@
 // (O's upper 64 rows are valid for group 0's channels, the lower for group 1's: half of the product is
 // thrown away, which costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
 // reference of each row, and their products with a group's scales have a factor of the row's and group's own; both
-// move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay in registers, 32 rows a thread, until the unit ends.
+// move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay in registers, 16 rows a thread, until the unit ends.
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
 // x 4 heads x 33,024 keys, 49 rows, 368 us (four blocks of 16 rows in kv4_attn.cu: 727 us; 403 where a thread
@@ -120,7 +120,7 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
                : "memory");
 }
 
-// Position p of eight in an operand holds code (channel of the word) kPerm(p): the order in which masks
+// Position p of eight in an operand holds code (channel of the word) perm8(p): the order in which masks
 // take codes out of a word, (0, 4), (1, 5), (2, 6), (3, 7); the second and fourth pair come at 2^-20.
 __device__ __forceinline__ constexpr int perm8(int p) { return (p >> 1) + 4 * (p & 1); }
 
@@ -133,7 +133,7 @@ __device__ __forceinline__ void widen_word(uint32_t x, uint32_t* r) {
 }
 // Half of a thread's key of K to tensor memory (its lane), 16 columns a group.
 template <int D>
-__device__ __forceinline__ void widen_k(uint32_t row, uint32_t taddr, int key, int part) {
+__device__ __forceinline__ void widen_k(uint32_t row, uint32_t taddr, int part) {
   uint32_t r[16];
   if constexpr (D == 64) {
     const uint4 v = lds128(row + 16 * part);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
     const bool k_side = wg == 0 || wg == 3;
     auto widen_keys = [&](int i) {
       if (k_side) {
-        widen_k<D>(stage_of(i) + key * At::CW, lanes + C::K + (i & 1) * GR * 32, key, wg == 3);
+        widen_k<D>(stage_of(i) + key * At::CW, lanes + C::K + (i & 1) * GR * 32, wg == 3);
         tc::tmem_st_wait();
       }
     };

@@ -62,6 +62,20 @@ def test_zeros_keep_their_signs_without_norm_and_rotation():
     assert torch.equal(q[0, 0].view(torch.int32), c["q"][0, 0].transpose(0, 1).contiguous().view(torch.int32))
 
 
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (128, torch.float32), (32, torch.float32)])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_entries_of_the_largest_stated_size_are_normalised(d, dtype, rows):
+    c = _make(1, 2, rows, 4, 2, d, dtype, [3, 0], d, 1, 4, fused=False)
+    for x in "qk":
+        c[x].mul_(2.0 ** 55)
+        c[x][0, 0, 0, 1] = torch.sign(c[x][0, 0, 0, 1].float()).to(dtype) * 2.0 ** 60
+        assert c[x].abs().max() == 2.0 ** 60
+    q, k, v, cv = _run(c)
+    cv.check()
+    assert B.std_get_device_error() == 0
+    _check(c, q, k, v)
+
+
 # ----------------------------------------------------------------------------- grids
 
 def _grid(tokens, rows, heads, sms):
