@@ -47,7 +47,9 @@ def _on(stream):
     current one)."""
     if stream is None:
         return nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):  # (ExternalStream(0) would be a stream of its own)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class Kv4Session:

@@ -121,3 +121,22 @@ def test_rounds_on_another_stream_and_in_a_graph(handle):
         assert torch.equal(io[x], want[x])
     assert all(torch.equal(a, b) for a, b in zip(_copy4(u), want4))
     assert B.std_get_device_error(clear=True) == 0
+
+
+def test_a_handle_of_zero_is_the_default_stream():
+    """A round on 0, called while another stream is current, comes after what the default stream holds."""
+    s = _session([100, 61, 0])
+    io, tokens = _io(s, 10, [0, 0, 0]), _io(s, 10, [2, 4, 0])["dense_tokens"]
+    s.round(io, stream=0)                        # (first calls load kernels and take memory, which waits for the device)
+    s.start([100, 61, 0])
+    side = torch.cuda.Stream()
+    busy = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(600):                         # (some 50 ms, well above what the round takes to be launched)
+        busy.add_(1)
+    io["dense_tokens"].copy_(tokens)
+    with torch.cuda.stream(side):
+        s.round(io, stream=0)
+    torch.cuda.synchronize()
+    assert s.len_full.tolist() == [103, 66, 1]
+    assert B.std_get_device_error(clear=True) == 0
