@@ -142,7 +142,6 @@ __device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {  // (a predic
 // neighbouring rows for the quad, and the K rows of neighbouring g lie in different banks.
 template <int D, int NT, bool F32>
 struct State {
-  static constexpr int KS = D / 16;          // k-steps of S^T
   static constexpr int GR = D / kKv4Group;   // groups
   static constexpr int MT = D / 16;          // 16-channel tiles of O^T
   // The queries, each row scaled by a power of two, are B operands in shared memory, four registers of a lane
@@ -262,16 +261,17 @@ __device__ __forceinline__ void load_queries(State<D, NT, F32>& st, const Kv4Att
 template <int D, int NT, bool F32>
 __device__ __forceinline__ void settle(State<D, NT, F32>& st) {
   using S = State<D, NT, F32>;
-  if constexpr (F32) return;
+  if constexpr (!F32) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] -= st.eight[F32 ? 0 : nt][mt / 4][i];
+        for (int mt = 0; mt < S::MT; ++mt) st.o[nt][mt][i] -= st.eight[nt][mt / 4][i];
 #pragma unroll
-      for (int gr = 0; gr < S::GR; ++gr) st.eight[F32 ? 0 : nt][gr][i] = 0.f;
-    }
+        for (int gr = 0; gr < S::GR; ++gr) st.eight[nt][gr][i] = 0.f;
+      }
+  }
 }
 
 // A lane's byte offsets into shared memory: everything it reads of a warp's 16 rows lies at one of
@@ -412,7 +412,10 @@ __device__ __forceinline__ void attend16(State<D, NT, F32>& st, const LaneAt<D, 
     for (int e = 0; e < 2; ++e) l[nt][e] = st.l[nt][e] + (p[nt][e] + p[nt][2 + e]);
   };
   auto times_scale = [&](int nt, int gr, int i) {  // (a scale past the limit may be anything)
-    return MASK && !seen[nt][i] ? 0.f : p[nt][i] * sv[i >> 1][gr];
+    if constexpr (MASK) {
+      if (!seen[nt][i]) return 0.f;
+    }
+    return p[nt][i] * sv[i >> 1][gr];
   };
   auto weigh = [&](int nt) {
 #pragma unroll

@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
         const bool mine = tid < kRows && (tid & ~7) < live;  // (rows behind the last share its eight)
         // every row's largest logit, first over the warps
         each_logit([&](int row, float x, bool seen) {
-          const float z = warp_max(seen ? x * tab[5 * kRows + row] : -INFINITY);
+          const float z = warp_max_f32(seen ? x * tab[5 * kRows + row] : -INFINITY);
           if (lane == 0) red[2 * (qd * kRows + row)] = z;
         });
         __syncthreads();
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnA
           const float w = seen ? ex2(fmaf(x, tab[5 * kRows + row], tab[2 * kRows + row])) : 0.f;
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr) {
-            const float top = warp_max(seen ? w * sv[gr] : 0.f);
+            const float top = warp_max_f32(seen ? w * sv[gr] : 0.f);
             if (lane == 0) red[2 * (qd * kRows + row) + gr] = top;
           }
         });
