@@ -30,9 +30,10 @@
 // with a softmax state of its own.  The states merge once for each unit a CTA touches; units that several
 // CTAs touch merge in a second kernel.
 //
-// Measured: 28 layers x 4 heads x 143,616 keys, 7 rows, 460 us, 5.0 TB/s of 6.46.  16 keys are
-// 305 instructions of a warp; with the 16 warps that 126 registers leave an SM, 57% of the issue slots and 53%
-// of the integer pipe are used: four warps a scheduler do not hide their own latencies.
+// Measured: 28 layers x 4 heads x 143,616 keys, 7 rows, 495 to 538 us a call among many, where the power cap holds the
+// clock at some 1,740 MHz (4.3 to 4.7 TB/s of 6.46), 460 us in a short sequence at 1,965.  16 keys are 312 instructions
+// of a warp; with the 16 warps that 128 registers leave an SM, 59% of the issue slots and 53% of the integer pipe
+// are used: four warps a scheduler do not hide their own latencies.
 #include "kv4_attn.cuh"
 
 #include <atomic>
@@ -732,8 +733,8 @@ cudaError_t launch(const Kv4AttnArgs& a, cudaStream_t s) {
 
 // More than 16 query rows share a widened code often enough for the tensor-memory kernel (bf16; fp32
 // queries need their second fp16 term, and two weights for one, and stay here).  28 layers x 4 heads x
-// 33,024 keys, there / here: 16 rows 288 / 192 us, 18 rows 296 / 370, 28 rows 332 / 373, 49 rows 367 / 727.
-// (One layer of 16,512 keys: 18 rows 18.2 / 17.9, 28 rows 18.9 / 18.6, 49 rows 21.9 / 24.6.)
+// 33,024 keys, there / here: 16 rows 301 / 198 us, 18 rows 310 / 380, 28 rows 353 / 383, 49 rows 393 / 748.
+// (One layer of 16,512 keys: 18 rows 18.8 / 18.1, 28 rows 19.8 / 18.9, 49 rows 23.1 / 25.2.)
 static bool on_tensor_memory(const Kv4AttnArgs& a) { return a.dtype == STD_BF16 && a.rows > 16; }
 
 // Query rows of a block, and CTAs of an SM, by the kernel the call takes.

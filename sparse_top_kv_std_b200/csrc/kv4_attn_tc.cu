@@ -13,8 +13,9 @@
 // move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay in registers, 16 rows a thread, until the unit ends.
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
-// x 4 heads x 33,024 keys, 49 rows, 368 us (four blocks of 16 rows in kv4_attn.cu: 727 us; 403 where a thread
-// widens a group of its key of K and not half a row, which reads all codes twice).  Of a tile's 3,350 clocks the tensor cores are busy 800; the phases follow each other.
+// x 4 heads x 33,024 keys, 49 rows, 394 us (four blocks of 16 rows in kv4_attn.cu: 748 us; without the factors of rows
+// and groups 372, and 403 where a thread widened a group of its key of K and not half a row, which reads all codes
+// twice).  Of a tile's 3,490 clocks the tensor cores are busy 770; the phases follow each other.
 #include "kv4_attn.cuh"
 
 #include <atomic>
@@ -28,8 +29,8 @@ constexpr int kThreads = kTile * kRows / kShare;
 constexpr int kStages = 4;
 // The thread that fetches tiles, and the warps that issue the products: of those that widen K, which is less
 // work than V.  (The issue of P V blocks its warp until the tensor cores have taken most of it, some 800
-// clocks; wg 3 has the fewest rows where a block is short.  On the S issuer's scheduler, warp 12, it is 377 us
-// where this is 368.)
+// clocks; wg 3 has the fewest rows where a block is short.  On the S issuer's scheduler, warp 12, it is 412 us
+// where this is 400.)
 constexpr int kFetcher = kThreads - 32, kIssueS = 0, kIssuePV = 13;
 static_assert(kIssueS != kIssuePV && kIssueS != kFetcher / 32 && kIssuePV != kFetcher / 32, "one role a warp");
 constexpr float kMostWeight = 1.1529215e18f;  // 2^60: a weight above it moves its reference, however small the scales
