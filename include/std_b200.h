@@ -593,12 +593,12 @@ size_t std_kv4_attn_workspace_size(const std_dims* dims, int q_rows, int64_t cap
  *    STD_DEVERR_LENGTH and leaves that sequence's o as it is.  A row that attends no key gets o = 0.
  * Keys, values, softmax statistics and sums are those of the cache's values in float32 arithmetic; for
  * bf16 queries a weight is rounded once to 11 bits where it enters the tensor cores, for fp32 queries
- * it and the query keep 22 -- or, where that is more, 2^-32 of the row's largest product of a weight and a value
- * scale in that group of 64 channels, whatever the sizes of the other group and the other rows.  A query row does not depend on the others: whatever they hold, its entries keep
- * their bits (bf16 down to 2^-27 of the row's largest, fp32 22 of them down to 2^-17) or, below that, are off by
- * at most 2^-35 of the row's largest.  Sums of weights times values are divided at the end: they cannot overflow
- * for values up to 2^40 and queries up to 2^100 in magnitude, whatever the lengths, and keep their bits for
- * values down to 2^-80.
+ * it and the query keep 22 -- or, where that is more, 2^-32 of the row's largest product of a weight and a
+ * value scale in that group of 64 channels, whatever the sizes of the other group and the other rows.  A query
+ * row does not depend on the others: whatever they hold, its entries keep their bits (bf16 down to 2^-27 of
+ * the row's largest, fp32 22 of them down to 2^-17) or, below that, are off by at most 2^-35 of the row's
+ * largest.  Sums of weights times values are divided at the end: they cannot overflow for values up to 2^40
+ * and queries up to 2^100 in magnitude, whatever the lengths, and keep their bits for values down to 2^-80.
  * Requires 1 <= q_rows <= 32, G * q_rows <= 128, B <= 1024, d 64 or 128.  The workspace needs no
  * initial value; calls that may overlap on the device need workspaces of their own. */
 int std_kv4_attn(const std_dims* dims, const void* q, int q_rows, const std_kv4_cache* cache, const int32_t* len,

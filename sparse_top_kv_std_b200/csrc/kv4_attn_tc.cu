@@ -7,10 +7,11 @@
 //   O [2 x 64 rows][128 channels] += (P sv_0 over P sv_1) x V codes (both shared memory, read across their rows)
 // With keys in the lanes of S a key's scales and minima are a thread's own: it turns its part of S_0 and S_1
 // into logits and weights, multiplies them by sv_0 and sv_1 and writes 16-bit rows of the next operand.
-// (O's upper 64 rows are valid for group 0's channels, the lower for group 1's: half of the product is
-// thrown away, which costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
+// (O's upper 64 rows are valid for group 0's channels, the lower for group 1's: half of the product is thrown away,
+// which costs what two half-height products would.)  No maximum is taken on the way: weights are relative to a
 // reference of each row, and their products with a group's scales have a factor of the row's and group's own; both
-// move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay in registers, 16 rows a thread, until the unit ends.
+// move only when some product would leave fp16's range, so a tile has one barrier, and the sums of p and p m stay
+// in registers, 16 rows a thread, until the unit ends.
 //
 // A tile at d = 128 is 18 KB; at full HBM rate it would be 760 clocks.  Measured: 28 layers
 // x 4 heads x 33,024 keys, 49 rows, 394 us (four blocks of 16 rows in kv4_attn.cu: 748 us; without the factors of rows
